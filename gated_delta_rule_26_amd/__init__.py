@@ -15,6 +15,9 @@ Entry points (same names as the C ABI):
   chunk_bwd(q, k, v, g, beta, d_o, ...)   -> dict of gradients  backward pass (training)
   chunk_fwd_noalloc(q, k, v, g, beta, o, ...) -> o         chunked prefill, no device allocation
   chunk_fwd_workspace_size(...)           -> bytes
+and, from ``ops.py``: head_decay_fwd, head_decay_bwd (each also _varlen) and
+head_decay_step (linear attention with one decay per head), beam_select and
+beam_reorder (beam search over decode steps).
 """
 from __future__ import annotations
 
@@ -107,6 +110,19 @@ def load_library(path: str | None = None):
     lib.gdr_recurrent_fwd_varlen.argtypes = [D, V, V, V, V, V, V, V, V, V]
     lib.gdr_chunk_fwd_noalloc.restype = ctypes.c_int
     lib.gdr_chunk_fwd_noalloc.argtypes = [D, V, V, V, V, V, V, V, V, V]
+    I, L, Z = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    for name, args in {
+            "gdr_head_decay_fwd_workspace_size": [V, ctypes.c_int, ctypes.POINTER(Z)],
+            "gdr_head_decay_fwd": [V] * 10 + [Z, V],
+            "gdr_head_decay_bwd_workspace_size": [V, ctypes.c_int, ctypes.c_int, ctypes.POINTER(Z)],
+            "gdr_head_decay_bwd": [V] * 15 + [Z, V],
+            "gdr_head_decay_step": [V] * 6 + [I] + [V] * 5,
+            "gdr_beam_select_workspace_size": [I, I, I, ctypes.POINTER(Z)],
+            "gdr_beam_select": [I, I, I, I, V, L, V, V, I, I, V, V, V, V, V, Z, V],
+            "gdr_beam_reorder": [I, I, I, L, V, V, V, V]}.items():
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = args
     if path is None:
         _lib = lib
     return lib
@@ -628,3 +644,12 @@ def chunk_fwd_noalloc(q, k, v, g, beta, o, *, s0=None, s_final=None, per_channel
     if rc != 0:
         raise GdrError(rc, "gdr_chunk_fwd_noalloc")
     return o, s_final
+
+
+from .ops import (HeadDecayDesc, beam_reorder, beam_select, beam_select_workspace_size,  # noqa: E402
+                  head_decay_bwd, head_decay_bwd_varlen, head_decay_bwd_workspace_size, head_decay_fwd,
+                  head_decay_fwd_varlen, head_decay_fwd_workspace_size, head_decay_step, make_head_decay_desc)
+
+__all__ += ["HeadDecayDesc", "beam_reorder", "beam_select", "beam_select_workspace_size", "head_decay_bwd",
+            "head_decay_bwd_varlen", "head_decay_bwd_workspace_size", "head_decay_fwd", "head_decay_fwd_varlen",
+            "head_decay_fwd_workspace_size", "head_decay_step", "make_head_decay_desc"]

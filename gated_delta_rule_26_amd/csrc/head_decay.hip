@@ -1,0 +1,760 @@
+// Linear attention with one decay per head: the chunked forward and backward passes.
+//
+// Every product of the family is one walk (struct Walk, ops_internal.h): with lambda = exp(g_h), walk order
+// i, j = 0 .. n-1 inside a chunk, and the fp32 state E,
+//   out_i = oscale lambda^i E^T a_i + pscale sum_{j<=i} lambda^{i-j} (a_i . b_j) c_j
+//   E'    = lambda^n E + uscale sum_j lambda^{n-j} b_j c_j^T
+// which is o (a, b, c = q, k, v), dq (d_o, v, k), and in reversed time dv (k, q, d_o) and dk (v, d_o, q).
+//
+// Long sequences are cut into segments, so that a few heads fill the card: the first kernel sums each
+// segment's writes from a zero state, U = sum_j lambda^{len-j} b_j c_j^T (exactly the walk without outputs),
+// and the walk of segment s starts from E = lambda^len E + U over the segments before it.
+//
+// One workgroup of four wavefronts walks one segment of one head and a slice of c's columns, 16 NT of them
+// per wavefront, so that the state never leaves the registers: the 16x16 tiles of E that the update's MFMAs
+// accumulate (rows: a's channels, columns: c's) are, lane by lane, the operand of the state's read, when the
+// read's other operand is taken in the permuted order of matrix_common.h.  The pair matrix is shared: its
+// lower 16x16 tiles are spread over the wavefronts, which exchange them through LDS as operand fragments.
+// All outputs are formed transposed (rows: c's channels, columns: tokens), so that the decay of a token is a
+// factor per lane, and the columns of a wavefront's tiles are interleaved so that a lane holds 4 NT
+// consecutive channels of a token: one 16-byte store.
+//
+// Roundings below fp32 with bf16 inputs (products of bf16 values are exact in fp32): the pair matrix is
+// rounded to bf16 before it meets c (relative 2^-9 per pair, of the size of the output's own rounding);
+// the state and the decayed c of the update are split into bf16 hi + lo (2^-17), since the state is fp32
+// for the caller and its errors would add up over the chunks.  With fp32 inputs all products are fp32 MFMAs.
+#include "matrix_common.h"
+#include "ops_internal.h"
+
+namespace gdr {
+namespace hd {
+namespace {
+
+using mx::bf16x4;
+using mx::bf16x8;
+using mx::f32x4;
+
+__device__ __forceinline__ float decay_power(float g, int x) { return x == 0 ? 1.f : expf(static_cast<float>(x) * g); }
+
+// Inclusive scan over the workgroup's 256 threads; `tmp` holds 4 values.  Two barriers.
+template <bool MAX>
+__device__ int block_scan(int x, int *tmp) {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int y = __shfl_up(x, off, 64);
+        if (lane >= off) x = MAX ? max(x, y) : x + y;
+    }
+    __syncthreads();
+    if (lane == 63) tmp[w] = x;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (i < w) x = MAX ? max(x, tmp[i]) : x + tmp[i];
+    return x;
+}
+
+// Where segment unit u lies: sequence n (-1: none), its first token's row tok0 (0 in a fixed-length batch)
+// and length, the segment's number s of ns and its tokens [t0, t0 + len) of the sequence.  first, last: the
+// rows that the sequences of a packed batch cover (unit 0 only).  chunk0: the number of the segment's first
+// chunk among those of all sequences, where COUNT asks for it.
+struct Place {
+    int n, tok0, seq_len, s, ns, t0, len, first, last, chunk0;
+};
+
+struct PlaceSmem {
+    int tmp[4];
+    int found[6];
+};
+
+template <int CH, bool COUNT>
+__device__ Place find_place(const Batch &b, int u, PlaceSmem &sm) {
+    Place p;
+    p.first = 0;
+    p.last = b.T;
+    if (!b.cu) {
+        p.n = u / b.per_seq;
+        p.s = u - p.n * b.per_seq;
+        p.ns = b.per_seq;
+        p.tok0 = 0;
+        p.seq_len = b.T;
+        p.chunk0 = p.n * ((b.T + CH - 1) / CH);
+    } else {
+        // offsets clamped to [0, T] and raised to the largest before them; sequence i owns
+        // max(1, ceil(len / seg)) units
+        const int t = threadIdx.x;
+        if (t == 0) sm.found[0] = -1;
+        int top = 0, units = 0, chunks = 0;
+        p.first = min(max(b.cu[0], 0), b.T);
+        for (int base = 0; base < b.N; base += kThreads) {
+            const int i = base + t;
+            const int lo = i <= b.N ? min(max(b.cu[i], 0), b.T) : 0;
+            const int hi = i < b.N ? min(max(b.cu[i + 1], 0), b.T) : 0;
+            const int start = max(top, block_scan<true>(lo, sm.tmp));
+            const int end = max(start, hi);
+            const int mine = i < b.N ? max(1, (end - start + b.seg - 1) / b.seg) : 0;
+            const int upto = units + block_scan<false>(mine, sm.tmp);
+            const int own = i < b.N ? (end - start + CH - 1) / CH : 0;
+            int chunks_to = 0;
+            if constexpr (COUNT) chunks_to = chunks + block_scan<false>(own, sm.tmp);
+            if (i < b.N && u >= upto - mine && u < upto) {
+                sm.found[0] = i;
+                sm.found[1] = start;
+                sm.found[2] = end - start;
+                sm.found[3] = u - (upto - mine);
+                sm.found[4] = mine;
+                sm.found[5] = chunks_to - own;
+            }
+            __syncthreads();  // the scans' last reads of tmp are done
+            if (t == kThreads - 1) {
+                sm.tmp[0] = max(start, end);
+                sm.tmp[1] = upto;
+                sm.tmp[2] = chunks_to;
+            }
+            __syncthreads();
+            top = sm.tmp[0];
+            units = sm.tmp[1];
+            chunks = sm.tmp[2];
+            if (u > 0 && u < units) break;
+        }
+        __syncthreads();
+        p.last = top;
+        p.n = sm.found[0];
+        p.tok0 = sm.found[1];
+        p.seq_len = sm.found[2];
+        p.s = sm.found[3];
+        p.ns = sm.found[4];
+        p.chunk0 = sm.found[5];
+        if (p.n < 0) return p;
+    }
+    p.t0 = p.s * b.seg;
+    p.len = min(b.seg, p.seq_len - p.t0);
+    p.chunk0 += p.t0 / CH;
+    return p;
+}
+
+// ---- element types: operand fragments of `depth` terms; term e of lane group lg (lane / 16) is term
+// kperm(lg, e) of a 32-block (bf16) or 4 lg + e of a 16-block (fp32).
+template <bool BF16>
+struct El;
+template <>
+struct El<true> {
+    static constexpr int bytes = 2, depth = 32, ldpad = 8;
+    using frag = bf16x8;
+    using half = bf16x4;  // what one 16x16 tile gives to a fragment
+    typedef __bf16 lds;
+};
+template <>
+struct El<false> {
+    static constexpr int bytes = 4, depth = 16, ldpad = 4;
+    using frag = f32x4;
+    using half = f32x4;
+    typedef float lds;
+};
+
+__device__ __forceinline__ f32x4 mul_add(bf16x8 a, bf16x8 b, f32x4 c) { return mx::mma(a, b, c); }
+__device__ __forceinline__ f32x4 mul_add(f32x4 a, f32x4 b, f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = mx::mma32(a[e], b[e], c);
+    return c;
+}
+
+// ---- a tile of ROWS tokens x W channels: global -> registers -> LDS, 16 bytes a lane
+template <bool BF16, int W, int ROWS>
+struct Tile {
+    using T = El<BF16>;
+    static constexpr int per = 16 / T::bytes;       // elements of a piece
+    static constexpr int pieces = W / per;          // of a row
+    static constexpr int rpp = kThreads / pieces;   // rows of a pass
+    static constexpr int passes = ROWS / rpp;
+    static constexpr int ld = W + T::ldpad;
+    static_assert(kThreads % pieces == 0 && ROWS % rpp == 0, "tile must divide among the threads");
+    uint4 r[passes];
+
+    // rows 0 .. n-1 of `stride` bytes from `p` on, channels col0 .. col0 + W - 1 of `width`; zeros elsewhere
+    __device__ __forceinline__ void load(const char *p, int64_t stride, int n, int col0, int width) {
+        const int pc = threadIdx.x % pieces, r0 = threadIdx.x / pieces;
+        const int col = col0 + pc * per;
+        const char *at = p + r0 * stride + (int64_t)col * T::bytes;
+#pragma unroll
+        for (int i = 0; i < passes; ++i) {
+            const bool ok = r0 + i * rpp < n && col < width;
+            r[i] = make_uint4(0, 0, 0, 0);
+            if (ok) r[i] = *reinterpret_cast<const uint4 *>(at + (int64_t)(i * rpp) * stride);
+        }
+    }
+    // PERM: bf16 channels of each 32-block in the order of kperm, so that a 16-byte read is a fragment
+    template <bool PERM>
+    __device__ __forceinline__ void store(typename T::lds *s) const {
+        const int pc = threadIdx.x % pieces, r0 = threadIdx.x / pieces;
+#pragma unroll
+        for (int i = 0; i < passes; ++i) {
+            typename T::lds *row = s + (r0 + i * rpp) * ld;
+            if constexpr (BF16 && PERM) {
+                *reinterpret_cast<uint2 *>(row + mx::kperm_col(pc, 0)) = make_uint2(r[i].x, r[i].y);
+                *reinterpret_cast<uint2 *>(row + mx::kperm_col(pc, 1)) = make_uint2(r[i].z, r[i].w);
+            } else {
+                *reinterpret_cast<uint4 *>(row + pc * per) = r[i];
+            }
+        }
+    }
+};
+
+// Fragment of row `row`, block kb of channels (tile staged with PERM).
+template <bool BF16>
+__device__ __forceinline__ typename El<BF16>::frag row_frag(const typename El<BF16>::lds *s, int ld, int row, int kb,
+                                                            int lg) {
+    if constexpr (BF16) return *reinterpret_cast<const bf16x8 *>(s + row * ld + 32 * kb + 8 * lg);
+    else return *reinterpret_cast<const f32x4 *>(s + row * ld + 16 * kb + 4 * lg);
+}
+// Fragment over tokens (block kb of them) of channel 16 t + lr (tile staged with PERM).
+template <bool BF16>
+__device__ __forceinline__ typename El<BF16>::frag col_frag(const typename El<BF16>::lds *s, int ld, int t, int kb,
+                                                            int lr, int lg) {
+    if constexpr (BF16) {
+        return mx::kt_operand(s, ld, t, kb, lr, lg);
+    } else {
+        f32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = s[(16 * kb + 4 * lg + e) * ld + 16 * t + lr];
+        return x;
+    }
+}
+// Fragment over tokens of the column that lane lr has in column tile nt of NT interleaved ones (tile staged
+// as it is; col0: the wavefront's first column).
+template <bool BF16, int NT>
+__device__ __forceinline__ typename El<BF16>::frag c_frag(const typename El<BF16>::lds *s, int ld, int col0, int nt,
+                                                          int kb, int lr, int lg) {
+    if constexpr (BF16) {
+        const int col = col0 + 4 * NT * (lr & 3) + 4 * nt;
+        const int row = 32 * kb + 4 * lg + (lr >> 2);
+        const bf16x4 a = mx::lds_read_tr(s + row * ld + col);
+        const bf16x4 c = mx::lds_read_tr(s + (row + 16) * ld + col);
+        return bf16x8{a[0], a[1], a[2], a[3], c[0], c[1], c[2], c[3]};
+    } else {
+        f32x4 x;
+        const int col = col0 + 4 * NT * (lr >> 2) + 4 * nt + (lr & 3);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = s[(16 * kb + 4 * lg + e) * ld + col];
+        return x;
+    }
+}
+
+enum { kSums = 0, kWalk = 1, kWalkDg = 2 };
+
+template <bool BF16, int PAD, int NT, int CH, int MODE>
+struct Smem {
+    using L = typename El<BF16>::lds;
+    static constexpr int nfrag = BF16 ? (CH / 16) * (CH / 32) : (CH / 16) * (CH / 16);
+    __align__(16) L a[MODE == kSums ? 1 : CH * Tile<BF16, PAD, CH>::ld];
+    __align__(16) L b[CH * Tile<BF16, PAD, CH>::ld];
+    __align__(16) L c[CH * Tile<BF16, 64 * NT, CH>::ld];
+    __align__(16) char p[MODE == kSums ? 16 : nfrag * 1024];
+    __align__(16) char ph[MODE == kWalkDg ? nfrag * 1024 : 16];  // (i - j) times the pair matrix, hi
+    __align__(16) char pl[MODE == kWalkDg ? nfrag * 1024 : 16];  // and lo
+    __align__(16) float rpow[2 * CH + 8];                        // lambda^(CH - y), 0 behind
+    double dg[4];
+    PlaceSmem place;
+};
+
+template <bool BF16, int PAD, int NT, int CH, int MODE>
+__global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
+    using T = El<BF16>;
+    using frag = typename T::frag;
+    constexpr int KD = PAD / T::depth;   // channel blocks of a row
+    constexpr int KT = CH / T::depth;    // token blocks of a chunk
+    constexpr int CI = CH / 16;          // token tiles of a chunk
+    constexpr int TT = PAD / 16;         // row tiles of the state
+    constexpr int COLS = 64 * NT;
+    constexpr bool OUT = MODE != kSums, DG = MODE == kWalkDg;
+    using TileA = Tile<BF16, PAD, CH>;
+    using TileC = Tile<BF16, COLS, CH>;
+    constexpr int LDA = TileA::ld, LDC = TileC::ld;
+    __shared__ Smem<BF16, PAD, NT, CH, MODE> sm;
+
+    const Walk &w = set.w[blockIdx.y];
+    const Batch &b = set.b;
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, lr = lane & 15, lg = lane >> 4;
+    int group, slice;
+    mx::state_slot(blockIdx.x, b.units * b.H, set.slices, group, slice);
+    const int u = group / b.H, h = group - u * b.H;
+    const Place pl = find_place<CH, DG>(b, u, sm.place);
+    const size_t part = ((size_t)u * b.H + h) * set.slices + slice;  // of u, chunk_e, dg_part
+    const int col0 = slice * COLS + wv * 16 * NT;                    // the wavefront's first column
+    if (OUT && b.cu && w.zero_outside && u == 0) {
+        const int es = w.out_f32 ? 4 : T::bytes, per = 16 / es;
+        const int cols = min(COLS, w.Dc - slice * COLS);
+        const int outside = pl.first + (b.T - pl.last);
+        for (int x = tid; x < outside * (cols / per); x += kThreads) {
+            const int i = x / (cols / per), row = i < pl.first ? i : pl.last + (i - pl.first);
+            char *dst = w.out + (((int64_t)row * b.H + h) * w.Dc + slice * COLS + (x % (cols / per)) * per) * es;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (pl.n < 0 || slice * COLS >= w.Dc) {
+        if (DG && w.dg_part && tid == 0) w.dg_part[part] = 0.0;
+        return;
+    }
+
+    const bool last_seg = w.reverse ? pl.s == 0 : pl.s == pl.ns - 1;
+    if (!OUT && last_seg) return;  // no segment starts from its sum
+
+    const float g = b.g[h];
+    for (int y = tid; y < 2 * CH + 8; y += kThreads) sm.rpow[y] = y <= CH ? decay_power(g, CH - y) : 0.f;
+    auto lam = [&](int x) { return sm.rpow[CH - x]; };  // lambda^x, 0 <= x <= CH
+    if constexpr (OUT && BF16) {
+        // the upper tiles inside the fragments' 32-blocks stay zero
+        for (int x = tid; x < CI * KT * 64; x += kThreads) {
+            const int I = x / 64 / KT, kb = x / 64 % KT;
+            if (2 * kb + 1 > I) {
+                *reinterpret_cast<uint4 *>(sm.p + x * 16) = make_uint4(0, 0, 0, 0);
+                if constexpr (DG) {
+                    *reinterpret_cast<uint4 *>(sm.ph + x * 16) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(sm.pl + x * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- the entering state
+    const int mcol = 4 * NT * (lr >> 2) + (lr & 3);  // lane's column in tile 0 of the wavefront's columns
+    const size_t e_base = ((size_t)pl.n * b.H + h) * w.Da * w.Dc;
+    f32x4 E[TT][NT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) E[t][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto fragments = [&](float *base, size_t index, int t, int nt) {
+        return reinterpret_cast<f32x4 *>(base + index * (size_t)(PAD * COLS)) + ((wv * TT + t) * NT + nt) * 64 + lane;
+    };
+    if constexpr (OUT) {
+        if (w.e0) {
+            const float f = w.e0_decay ? lam(1) : 1.f;
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int row = 16 * t + 4 * lg, col = col0 + mcol + 4 * nt;
+                    if (row < w.Da && col < w.Dc) {
+                        if (w.e0_t) {
+                            E[t][nt] = *reinterpret_cast<const f32x4 *>(w.e0 + e_base + (size_t)col * w.Da + row);
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) E[t][nt][r] = w.e0[e_base + (size_t)(row + r) * w.Dc + col];
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) E[t][nt][r] *= f;
+                    }
+                }
+        }
+        const int before = w.reverse ? pl.ns - 1 - pl.s : pl.s;
+        for (int x = 0; x < before; ++x) {
+            const int s = w.reverse ? pl.ns - 1 - x : x;
+            const float f = decay_power(g, min(b.seg, pl.seq_len - s * b.seg));
+            const size_t index = ((size_t)(u - pl.s + s) * b.H + h) * set.slices + slice;
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const f32x4 add = *fragments(w.u, index, t, nt);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) E[t][nt][r] = f * E[t][nt][r] + add[r];
+                }
+        }
+    }
+
+    // ---- the walk
+    const int chunks = (pl.len + CH - 1) / CH;
+    const char *pa = nullptr, *pb, *pc;
+    const int64_t tok = pl.tok0 + pl.t0;
+    auto view = [&](const View &v) { return v.p + (b.cu ? 0 : pl.n * v.seq) + (h / v.div) * v.head + tok * v.tok; };
+    if constexpr (OUT) pa = view(w.a);
+    pb = view(w.b);
+    pc = view(w.c);
+    TileA ta, tb;
+    TileC tc;
+    auto fetch = [&](int x) {
+        const int ci = w.reverse ? chunks - 1 - x : x;
+        const int n = min(CH, pl.len - ci * CH);
+        const int64_t row = ci * CH + (w.reverse ? n - 1 : 0);
+        const int sgn = w.reverse ? -1 : 1;
+        if constexpr (OUT) ta.load(pa + row * w.a.tok, sgn * w.a.tok, n, 0, w.Da);
+        tb.load(pb + row * w.b.tok, sgn * w.b.tok, n, 0, w.Da);
+        tc.load(pc + row * w.c.tok, sgn * w.c.tok, n, slice * COLS, w.Dc);
+    };
+    const float pscale = w.oscale * w.uscale;
+    double dg = 0.0;
+    if (chunks > 0) fetch(0);
+    for (int x = 0; x < chunks; ++x) {
+        const int ci = w.reverse ? chunks - 1 - x : x;
+        const int n = min(CH, pl.len - ci * CH);
+        __syncthreads();  // the tiles of the chunk before are read
+        if constexpr (OUT) ta.template store<true>(sm.a);
+        tb.template store<true>(sm.b);
+        tc.template store<false>(sm.c);
+        if (x + 1 < chunks) fetch(x + 1);
+        __syncthreads();
+
+        if constexpr (OUT) {
+            // pair tiles (I, J), J <= I, transposed (rows: tokens j, columns: tokens i)
+            for (int t = wv; t < CI * (CI + 1) / 2; t += 4) {
+                const int I = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, J = t - I * (I + 1) / 2;
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kb = 0; kb < KD; ++kb)
+                    acc = mul_add(row_frag<BF16>(sm.b, LDA, 16 * J + lr, kb, lg),
+                                  row_frag<BF16>(sm.a, LDA, 16 * I + lr, kb, lg), acc);
+                f32x4 val, wgt;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int d = 16 * (I - J) + lr - 4 * lg - r;
+                    val[r] = d >= 0 ? acc[r] * (lam(max(d, 0)) * pscale) : 0.f;
+                    wgt[r] = val[r] * static_cast<float>(d);
+                }
+                if constexpr (BF16) {
+                    const int at = ((I * KT + (J >> 1)) * 64 + lane) * 16 + (J & 1) * 8;
+                    const bf16x4 v = {static_cast<__bf16>(val[0]), static_cast<__bf16>(val[1]),
+                                      static_cast<__bf16>(val[2]), static_cast<__bf16>(val[3])};
+                    *reinterpret_cast<bf16x4 *>(sm.p + at) = v;
+                    if constexpr (DG) {
+                        uint2 hi, lo;
+                        mx::split2(wgt[0], wgt[1], hi.x, lo.x);
+                        mx::split2(wgt[2], wgt[3], hi.y, lo.y);
+                        *reinterpret_cast<uint2 *>(sm.ph + at) = hi;
+                        *reinterpret_cast<uint2 *>(sm.pl + at) = lo;
+                    }
+                } else {
+                    const int at = ((I * CI + J) * 64 + lane) * 16;
+                    *reinterpret_cast<f32x4 *>(sm.p + at) = val;
+                    if constexpr (DG) *reinterpret_cast<f32x4 *>(sm.ph + at) = wgt;
+                }
+            }
+        }
+
+        f32x4 O[CI][NT];
+        if constexpr (OUT) {
+            // the state's read, transposed: rows c's channels, columns tokens
+#pragma unroll
+            for (int I = 0; I < CI; ++I)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) O[I][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < KD; ++kb) {
+                frag hi[NT], lo[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (BF16) mx::pair_split(E[2 * kb][nt], E[2 * kb + 1][nt], hi[nt], lo[nt]);
+                    else hi[nt] = E[kb][nt];
+                }
+#pragma unroll
+                for (int I = 0; I < CI; ++I) {
+                    const frag af = row_frag<BF16>(sm.a, LDA, 16 * I + lr, kb, lg);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        O[I][nt] = mul_add(hi[nt], af, O[I][nt]);
+                        if constexpr (BF16) O[I][nt] = mul_add(lo[nt], af, O[I][nt]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int I = 0; I < CI; ++I) {
+                const float f = lam(16 * I + lr) * w.oscale;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) O[I][nt][r] *= f;
+            }
+            __syncthreads();  // the pair matrix is written
+        }
+
+        const bool end = last_seg && x + 1 == chunks;       // nothing reads E after it but the caller
+        const int less = end && !w.reverse && OUT ? 1 : 0;  // S, not lambda S
+        const bool update = !OUT || !end || w.ef;
+        if constexpr (DG) {
+            if (w.chunk_e) {
+                const size_t index = ((size_t)(pl.chunk0 + ci) * b.H + h) * set.slices + slice;
+                float sum = 0.f;
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        f32x4 *at = fragments(w.chunk_e, index, t, nt);
+                        if (!w.reverse) {
+                            *at = E[t][nt];
+                        } else {
+                            const f32x4 e = *at;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) sum += e[r] * E[t][nt][r];
+                        }
+                    }
+                // pairs across the whole chunk: n lambda^n <S, R>, and the stored E is lambda S
+                if (w.reverse) dg += static_cast<double>(sum) * static_cast<double>(n * lam(n - 1));
+            }
+        }
+        if (update) {
+            const float f = lam(n - less);
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) E[t][nt][r] *= f;
+        }
+        f32x4 Y[DG ? CI : 1][NT];
+        if constexpr (DG)
+#pragma unroll
+            for (int I = 0; I < CI; ++I)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) Y[I][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (DG) {
+            // the state's part of <x, out>, token i weighted by its distance to the chunk's start (in the
+            // direction that the pairs decay)
+            if (w.x.p) {
+                float sum = 0.f;
+                const char *px = view(w.x);
+#pragma unroll
+                for (int I = 0; I < CI; ++I) {
+                    const int i = 16 * I + lr;
+                    if (i < n) {
+                        const int64_t row = ci * CH + (w.reverse ? n - 1 - i : i);
+                        const float f = static_cast<float>(w.reverse ? i : i + 1);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int col = col0 + 4 * NT * lg + 4 * nt;
+                            if (col < w.Dc) {
+                                const char *at = px + row * w.x.tok + (int64_t)col * T::bytes;
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) sum += f * load_in<BF16>(at, r) * O[I][nt][r];
+                            }
+                        }
+                    }
+                }
+                dg += static_cast<double>(sum);
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < KT; ++kb) {
+            frag cf[NT], wh[NT], wl[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) cf[nt] = c_frag<BF16, NT>(sm.c, LDC, wv * 16 * NT, nt, kb, lr, lg);
+            if constexpr (OUT) {
+#pragma unroll
+                for (int I = 0; I < CI; ++I) {
+                    if (BF16 ? kb <= (I >> 1) : kb <= I) {
+                        const int at = ((I * KT + kb) * 64 + lane) * 16;
+                        const frag pf = *reinterpret_cast<const frag *>(sm.p + at);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) O[I][nt] = mul_add(cf[nt], pf, O[I][nt]);
+                        if constexpr (DG) {
+                            if (w.x.p && !w.reverse) {
+                                const frag qh = *reinterpret_cast<const frag *>(sm.ph + at);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) Y[I][nt] = mul_add(cf[nt], qh, Y[I][nt]);
+                                if constexpr (BF16) {
+                                    const frag ql = *reinterpret_cast<const frag *>(sm.pl + at);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) Y[I][nt] = mul_add(cf[nt], ql, Y[I][nt]);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            if (update) {
+                // token j's write still decays n - less - j times
+                const float *wt = sm.rpow + (CH - n + less);
+                float wj[T::depth / 4];
+#pragma unroll
+                for (int e = 0; e < T::depth / 4; ++e) {
+                    const int j = T::depth * kb + (BF16 ? mx::kperm(lg, e) : 4 * lg + e);
+                    wj[e] = wt[j] * w.uscale;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (BF16) {
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = static_cast<float>(cf[nt][e]) * wj[e];
+                        mx::split8(y, wh[nt], wl[nt]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) wh[nt][e] = cf[nt][e] * wj[e];
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    const frag bt = col_frag<BF16>(sm.b, LDA, t, kb, lr, lg);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        E[t][nt] = mul_add(bt, wh[nt], E[t][nt]);
+                        if constexpr (BF16) E[t][nt] = mul_add(bt, wl[nt], E[t][nt]);
+                    }
+                }
+            }
+        }
+
+        if constexpr (OUT) {
+            const int64_t row0 = (int64_t)(b.cu ? 0 : (int64_t)pl.n * b.T) + tok + ci * CH;
+#pragma unroll
+            for (int I = 0; I < CI; ++I) {
+                const int i = 16 * I + lr, col = col0 + 4 * NT * lg;
+                if (i < n && col < w.Dc) {
+                    const int64_t at = ((row0 + (w.reverse ? n - 1 - i : i)) * b.H + h) * w.Dc + col;
+                    if (!BF16 || w.out_f32) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(w.out) + at + 4 * nt) = O[I][nt];
+                    } else {
+                        uint32_t v[2 * NT];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const mx::bf16x2 x0 = {static_cast<__bf16>(O[I][nt][0]), static_cast<__bf16>(O[I][nt][1])};
+                            const mx::bf16x2 x1 = {static_cast<__bf16>(O[I][nt][2]), static_cast<__bf16>(O[I][nt][3])};
+                            v[2 * nt] = __builtin_bit_cast(uint32_t, x0);
+                            v[2 * nt + 1] = __builtin_bit_cast(uint32_t, x1);
+                        }
+                        if constexpr (NT == 2)
+                            *reinterpret_cast<uint4 *>(w.out + at * 2) = make_uint4(v[0], v[1], v[2], v[3]);
+                        else
+                            *reinterpret_cast<uint2 *>(w.out + at * 2) = make_uint2(v[0], v[1]);
+                    }
+                    if constexpr (DG) {
+                        if (w.x.p && !w.reverse) {
+                            const char *px = view(w.x) + (int64_t)(ci * CH + i) * w.x.tok + (int64_t)col * T::bytes;
+                            float sum = 0.f;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) sum += load_in<BF16>(px, 4 * nt + r) * Y[I][nt][r];
+                            dg += static_cast<double>(sum);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    if constexpr (!OUT) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) *fragments(w.u, part, t, nt) = E[t][nt];
+    } else {
+        if (w.ef && last_seg) {
+            // an empty sequence keeps its state: E holds e0, decayed in the forward direction
+            const bool empty = pl.seq_len == 0;
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int row = 16 * t + 4 * lg, col = col0 + mcol + 4 * nt;
+                    if (row < w.Da && col < w.Dc) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const size_t at = e_base + (size_t)(row + r) * w.Dc + col;
+                            w.ef[at] = empty ? (w.e0 ? w.e0[at] : 0.f) : E[t][nt][r];
+                        }
+                    }
+                }
+        }
+        if constexpr (DG) {
+            if (w.dg_part) {
+#pragma unroll
+                for (int off = 32; off > 0; off >>= 1) dg += __shfl_xor(dg, off, 64);
+                if (lane == 0) sm.dg[wv] = dg;
+                __syncthreads();
+                if (tid == 0)
+                    w.dg_part[part] = (sm.dg[0] + sm.dg[1]) + (sm.dg[2] + sm.dg[3]);
+            }
+        }
+    }
+}
+
+template <bool BF16, int PAD, int NT, int CH, int MODE>
+hipError_t launch(const WalkSet &s, hipStream_t stream) {
+    const dim3 grid((unsigned)(s.b.units * s.b.H * s.slices), (unsigned)s.count);
+    hipLaunchKernelGGL((walk_kernel<BF16, PAD, NT, CH, MODE>), grid, dim3(kThreads), 0, stream, s);
+    return hipGetLastError();
+}
+
+template <int MODE>
+hipError_t dispatch(const WalkSet &s, bool bf16, const Shape &sh, hipStream_t stream) {
+    if (bf16) {
+        if (sh.pad == 64) return launch<true, 64, 1, 64, MODE>(s, stream);
+        if (sh.pad == 128) return launch<true, 128, 2, 64, MODE>(s, stream);
+        return launch<true, 256, 1, 32, MODE>(s, stream);
+    }
+    if (sh.pad == 64) return launch<false, 64, 1, 32, MODE>(s, stream);
+    if (sh.pad == 128) return launch<false, 128, 2, 32, MODE>(s, stream);
+    return launch<false, 256, 1, 32, MODE>(s, stream);
+}
+
+// ---- sums over the query heads of a group, and of dL/dg's parts
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void group_sum_kernel(const float *__restrict__ src, void *__restrict__ dst,
+                                                             size_t quads, int G, int D) {
+    const size_t x = (size_t)blockIdx.x * kThreads + threadIdx.x;
+    if (x >= quads) return;
+    const size_t row = x / (D / 4), col = x % (D / 4) * 4;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < G; ++i) {
+        const float4 y = *reinterpret_cast<const float4 *>(src + (row * G + i) * D + col);
+        sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
+    }
+    const size_t at = row * D + col;
+    store_out<BF16>(dst, at, sum.x);
+    store_out<BF16>(dst, at + 1, sum.y);
+    store_out<BF16>(dst, at + 2, sum.z);
+    store_out<BF16>(dst, at + 3, sum.w);
+}
+
+__global__ __launch_bounds__(kThreads) void dg_sum_kernel(const double *__restrict__ part, float *__restrict__ dg,
+                                                          int units, int H, int slices, int walks, size_t stride) {
+    __shared__ double red[kThreads];
+    const int h = blockIdx.x;
+    double sum = 0.0;
+    for (int w = 0; w < walks; ++w)
+        for (size_t x = threadIdx.x; x < (size_t)units * slices; x += kThreads)
+            sum += part[w * stride + ((x / slices) * H + h) * slices + x % slices];
+    red[threadIdx.x] = sum;
+    __syncthreads();
+    for (int off = kThreads / 2; off > 0; off >>= 1) {
+        if ((int)threadIdx.x < off) red[threadIdx.x] += red[threadIdx.x + off];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) dg[h] = static_cast<float>(red[0]);
+}
+
+}  // namespace
+
+Shape shape_of(bool bf16, int wide) {
+    if (wide <= 64) return Shape{64, bf16 ? 64 : 32, 64};
+    if (wide <= 128) return Shape{128, bf16 ? 64 : 32, 128};
+    return Shape{256, 32, 64};
+}
+size_t frag_bytes(const Shape &s, int slices) { return (size_t)s.pad * s.cols * slices * sizeof(float); }
+
+hipError_t launch_segment_sums(const WalkSet &s, bool bf16, const Shape &sh, hipStream_t stream) {
+    return dispatch<kSums>(s, bf16, sh, stream);
+}
+hipError_t launch_walks(const WalkSet &s, bool bf16, const Shape &sh, bool dg, hipStream_t stream) {
+    return dg ? dispatch<kWalkDg>(s, bf16, sh, stream) : dispatch<kWalk>(s, bf16, sh, stream);
+}
+hipError_t launch_group_sum(const float *src, void *dst, bool bf16, size_t rows, int G, int D, hipStream_t stream) {
+    const size_t quads = rows * (D / 4);
+    if (quads == 0) return hipSuccess;
+    const dim3 grid((unsigned)((quads + kThreads - 1) / kThreads));
+    if (bf16) hipLaunchKernelGGL(group_sum_kernel<true>, grid, dim3(kThreads), 0, stream, src, dst, quads, G, D);
+    else hipLaunchKernelGGL(group_sum_kernel<false>, grid, dim3(kThreads), 0, stream, src, dst, quads, G, D);
+    return hipGetLastError();
+}
+hipError_t launch_dg_sum(const double *part, float *dg, int units, int H, int slices, int walks, size_t stride,
+                         hipStream_t stream) {
+    hipLaunchKernelGGL(dg_sum_kernel, dim3((unsigned)H), dim3(kThreads), 0, stream, part, dg, units, H, slices, walks,
+                       stride);
+    return hipGetLastError();
+}
+
+}  // namespace hd
+}  // namespace gdr
