@@ -34,6 +34,8 @@ using mx::bf16x4;
 using mx::bf16x8;
 using mx::f32x4;
 
+constexpr int kFar = 0x60000000;  // a byte offset out of any chunk's range, steps of a chunk's rows added or not
+
 __device__ __forceinline__ float decay_power(float g, int x) { return x == 0 ? 1.f : expf(static_cast<float>(x) * g); }
 
 // Inclusive scan over the workgroup's 256 threads; `tmp` holds 4 values.  Two barriers.
@@ -139,16 +141,14 @@ template <bool BF16>
 struct El;
 template <>
 struct El<true> {
-    static constexpr int bytes = 2, depth = 32, ldpad = 8;
+    static constexpr int bytes = 2, depth = 32;
     using frag = bf16x8;
-    using half = bf16x4;  // what one 16x16 tile gives to a fragment
     typedef __bf16 lds;
 };
 template <>
 struct El<false> {
-    static constexpr int bytes = 4, depth = 16, ldpad = 4;
+    static constexpr int bytes = 4, depth = 16;
     using frag = f32x4;
-    using half = f32x4;
     typedef float lds;
 };
 
@@ -159,40 +159,63 @@ __device__ __forceinline__ f32x4 mul_add(f32x4 a, f32x4 b, f32x4 c) {
     return c;
 }
 
-// ---- a tile of ROWS tokens x W channels: global -> registers -> LDS, 16 bytes a lane
-template <bool BF16, int W, int ROWS>
+// ---- a tile of ROWS tokens x W channels: global -> registers -> LDS, 16 bytes a lane.  Orders of the channels
+// in LDS, so that both the 16-byte accesses of rows and the transposing reads of 4x16 blocks take every bank once:
+//   kRows     read by rows only.  bf16: each 32-block in the order of kperm, a fragment being one 16-byte read
+//   kBoth     read by rows and transposed: as they come
+//   kColumns  read transposed only, in column tiles of NT interleaved ones: the quads of each 16 NT channels
+//             sorted by tile
+// (bf16 rows of kBoth and kColumns are 8 words longer than a multiple of the banks: the 8 rows x 32 bytes of a
+// transposing read's half lie side by side.)
+enum Order { kRows, kBoth, kColumns };
+
+template <bool BF16, int W, int ROWS, Order ORD, int NT = 1>
 struct Tile {
     using T = El<BF16>;
     static constexpr int per = 16 / T::bytes;       // elements of a piece
     static constexpr int pieces = W / per;          // of a row
     static constexpr int rpp = kThreads / pieces;   // rows of a pass
     static constexpr int passes = ROWS / rpp;
-    static constexpr int ld = W + T::ldpad;
+    static constexpr int ld = W + (BF16 ? (ORD == kRows ? 8 : 16) : 4);
     static_assert(kThreads % pieces == 0 && ROWS % rpp == 0, "tile must divide among the threads");
     uint4 r[passes];
 
-    // rows 0 .. n-1 of `stride` bytes from `p` on, channels col0 .. col0 + W - 1 of `width`; zeros elsewhere
-    __device__ __forceinline__ void load(const char *p, int64_t stride, int n, int col0, int width) {
-        const int pc = threadIdx.x % pieces, r0 = threadIdx.x / pieces;
-        const int col = col0 + pc * per;
-        const char *at = p + r0 * stride + (int64_t)col * T::bytes;
+    // This thread's first byte of a chunk of `stride` bytes a row, out of any chunk's range where the channel
+    // is past `width`.
+    static __device__ __forceinline__ int first(int stride, int col0, int width) {
+        const int col = col0 + (int)(threadIdx.x % pieces) * per;
+        return col < width ? (int)(threadIdx.x / pieces) * stride + col * T::bytes : kFar;
+    }
+    // Rows 0 .. n-1 of the chunk at `p`, in this or (reverse) the other order.  The buffer's bounds give zeros
+    // past the width and (but for rows that overlap by their stride) for what lies behind the last row or, as
+    // an unsigned offset, before the first.
+    __device__ __forceinline__ void load(const char *p, int stride, int at, int n, int row_end, bool reverse) {
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), (short)0,
+                                                            (n - 1) * stride + row_end, 0x00020000);
+        uint32_t off = (uint32_t)at + (reverse ? (uint32_t)((n - 1) * stride) : 0u);
+        const uint32_t step = (uint32_t)(reverse ? -rpp * stride : rpp * stride);
 #pragma unroll
         for (int i = 0; i < passes; ++i) {
-            const bool ok = r0 + i * rpp < n && col < width;
-            r[i] = make_uint4(0, 0, 0, 0);
-            if (ok) r[i] = *reinterpret_cast<const uint4 *>(at + (int64_t)(i * rpp) * stride);
+            r[i] = mx::buf_ld16(rsrc, (int)off);
+            off += step;
         }
     }
-    // PERM: bf16 channels of each 32-block in the order of kperm, so that a 16-byte read is a fragment
-    template <bool PERM>
     __device__ __forceinline__ void store(typename T::lds *s) const {
         const int pc = threadIdx.x % pieces, r0 = threadIdx.x / pieces;
 #pragma unroll
         for (int i = 0; i < passes; ++i) {
             typename T::lds *row = s + (r0 + i * rpp) * ld;
-            if constexpr (BF16 && PERM) {
+            if constexpr (BF16 && ORD == kRows) {
                 *reinterpret_cast<uint2 *>(row + mx::kperm_col(pc, 0)) = make_uint2(r[i].x, r[i].y);
                 *reinterpret_cast<uint2 *>(row + mx::kperm_col(pc, 1)) = make_uint2(r[i].z, r[i].w);
+            } else if constexpr (ORD == kColumns && NT == 2) {
+                if constexpr (BF16) {
+                    typename T::lds *at = row + 32 * (pc >> 2) + 4 * (pc & 3);
+                    *reinterpret_cast<uint2 *>(at) = make_uint2(r[i].x, r[i].y);
+                    *reinterpret_cast<uint2 *>(at + 16) = make_uint2(r[i].z, r[i].w);
+                } else {
+                    *reinterpret_cast<uint4 *>(row + 32 * (pc >> 3) + 16 * (pc & 1) + 4 * ((pc & 7) >> 1)) = r[i];
+                }
             } else {
                 *reinterpret_cast<uint4 *>(row + pc * per) = r[i];
             }
@@ -200,44 +223,46 @@ struct Tile {
     }
 };
 
-// Fragment of row `row`, block kb of channels (tile staged with PERM).
-template <bool BF16>
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 c) {
+    return bf16x8{a[0], a[1], a[2], a[3], c[0], c[1], c[2], c[3]};
+}
+// Fragment of row `row`, channel block kb.
+template <bool BF16, Order ORD>
 __device__ __forceinline__ typename El<BF16>::frag row_frag(const typename El<BF16>::lds *s, int ld, int row, int kb,
                                                             int lg) {
-    if constexpr (BF16) return *reinterpret_cast<const bf16x8 *>(s + row * ld + 32 * kb + 8 * lg);
-    else return *reinterpret_cast<const f32x4 *>(s + row * ld + 16 * kb + 4 * lg);
+    if constexpr (!BF16) {
+        return *reinterpret_cast<const f32x4 *>(s + row * ld + 16 * kb + 4 * lg);
+    } else if constexpr (ORD == kRows) {
+        return *reinterpret_cast<const bf16x8 *>(s + row * ld + 32 * kb + 8 * lg);
+    } else {
+        const __bf16 *at = s + row * ld + 32 * kb + 4 * lg;
+        return join(*reinterpret_cast<const bf16x4 *>(at), *reinterpret_cast<const bf16x4 *>(at + 16));
+    }
 }
-// Fragment over tokens (block kb of them) of channel 16 t + lr (tile staged with PERM).
+// Fragment over the tokens of block kb, of the 16 channels from col on (as they lie in LDS: lane lr has col + lr).
 template <bool BF16>
-__device__ __forceinline__ typename El<BF16>::frag col_frag(const typename El<BF16>::lds *s, int ld, int t, int kb,
+__device__ __forceinline__ typename El<BF16>::frag col_frag(const typename El<BF16>::lds *s, int ld, int col, int kb,
                                                             int lr, int lg) {
     if constexpr (BF16) {
-        return mx::kt_operand(s, ld, t, kb, lr, lg);
+        const __bf16 *at = s + (32 * kb + 4 * lg + (lr >> 2)) * ld + col + 4 * (lr & 3);
+        return join(mx::lds_read_tr(at), mx::lds_read_tr(at + 16 * ld));
     } else {
         f32x4 x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = s[(16 * kb + 4 * lg + e) * ld + 16 * t + lr];
+        for (int e = 0; e < 4; ++e) x[e] = s[(16 * kb + 4 * lg + e) * ld + col + lr];
         return x;
     }
 }
-// Fragment over tokens of the column that lane lr has in column tile nt of NT interleaved ones (tile staged
-// as it is; col0: the wavefront's first column).
-template <bool BF16, int NT>
-__device__ __forceinline__ typename El<BF16>::frag c_frag(const typename El<BF16>::lds *s, int ld, int col0, int nt,
-                                                          int kb, int lr, int lg) {
-    if constexpr (BF16) {
-        const int col = col0 + 4 * NT * (lr & 3) + 4 * nt;
-        const int row = 32 * kb + 4 * lg + (lr >> 2);
-        const bf16x4 a = mx::lds_read_tr(s + row * ld + col);
-        const bf16x4 c = mx::lds_read_tr(s + (row + 16) * ld + col);
-        return bf16x8{a[0], a[1], a[2], a[3], c[0], c[1], c[2], c[3]};
-    } else {
-        f32x4 x;
-        const int col = col0 + 4 * NT * (lr >> 2) + 4 * nt + (lr & 3);
+
+// Eight fp32 values as three bf16 terms, 24 bits: x = hi + mid + lo to fp32's own rounding.
+__device__ __forceinline__ void split8x3(const float *x, bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
+    float rest[8];
+    hi = bf16x8{static_cast<__bf16>(x[0]), static_cast<__bf16>(x[1]), static_cast<__bf16>(x[2]),
+                static_cast<__bf16>(x[3]), static_cast<__bf16>(x[4]), static_cast<__bf16>(x[5]),
+                static_cast<__bf16>(x[6]), static_cast<__bf16>(x[7])};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = s[(16 * kb + 4 * lg + e) * ld + col];
-        return x;
-    }
+    for (int e = 0; e < 8; ++e) rest[e] = x[e] - static_cast<float>(hi[e]);
+    mx::split8(rest, mid, lo);
 }
 
 enum { kSums = 0, kWalk = 1, kWalkDg = 2 };
@@ -246,9 +271,9 @@ template <bool BF16, int PAD, int NT, int CH, int MODE>
 struct Smem {
     using L = typename El<BF16>::lds;
     static constexpr int nfrag = BF16 ? (CH / 16) * (CH / 32) : (CH / 16) * (CH / 16);
-    __align__(16) L a[MODE == kSums ? 1 : CH * Tile<BF16, PAD, CH>::ld];
-    __align__(16) L b[CH * Tile<BF16, PAD, CH>::ld];
-    __align__(16) L c[CH * Tile<BF16, 64 * NT, CH>::ld];
+    __align__(16) L a[MODE == kSums ? 1 : CH * Tile<BF16, PAD, CH, kRows>::ld];
+    __align__(16) L b[CH * Tile<BF16, PAD, CH, kBoth>::ld];
+    __align__(16) L c[CH * Tile<BF16, 64 * NT, CH, kColumns, NT>::ld];
     __align__(16) char p[MODE == kSums ? 16 : nfrag * 1024];
     __align__(16) char ph[MODE == kWalkDg ? nfrag * 1024 : 16];  // (i - j) times the pair matrix, hi
     __align__(16) char pl[MODE == kWalkDg ? nfrag * 1024 : 16];  // and lo
@@ -267,14 +292,16 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
     constexpr int TT = PAD / 16;         // row tiles of the state
     constexpr int COLS = 64 * NT;
     constexpr bool OUT = MODE != kSums, DG = MODE == kWalkDg;
-    using TileA = Tile<BF16, PAD, CH>;
-    using TileC = Tile<BF16, COLS, CH>;
-    constexpr int LDA = TileA::ld, LDC = TileC::ld;
+    using TileA = Tile<BF16, PAD, CH, kRows>;
+    using TileB = Tile<BF16, PAD, CH, kBoth>;
+    using TileC = Tile<BF16, COLS, CH, kColumns, NT>;
+    constexpr int LDA = TileA::ld, LDB = TileB::ld, LDC = TileC::ld;
     __shared__ Smem<BF16, PAD, NT, CH, MODE> sm;
 
     const Walk &w = set.w[blockIdx.y];
     const Batch &b = set.b;
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, lr = lane & 15, lg = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     int group, slice;
     mx::state_slot(blockIdx.x, b.units * b.H, set.slices, group, slice);
     const int u = group / b.H, h = group - u * b.H;
@@ -348,19 +375,33 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
                     }
                 }
         }
+    }
+    if constexpr (OUT) {
+        // the segments before this one, two of them in flight
         const int before = w.reverse ? pl.ns - 1 - pl.s : pl.s;
-        for (int x = 0; x < before; ++x) {
-            const int s = w.reverse ? pl.ns - 1 - x : x;
-            const float f = decay_power(g, min(b.seg, pl.seq_len - s * b.seg));
-            const size_t index = ((size_t)(u - pl.s + s) * b.H + h) * set.slices + slice;
+        auto number = [&](int x) { return w.reverse ? pl.ns - 1 - x : x; };
+        auto load_sum = [&](int x, f32x4 (&to)[TT][NT]) {
+            const size_t index = ((size_t)(u - pl.s + number(x)) * b.H + h) * set.slices + slice;
 #pragma unroll
             for (int t = 0; t < TT; ++t)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const f32x4 add = *fragments(w.u, index, t, nt);
+                for (int nt = 0; nt < NT; ++nt) to[t][nt] = *fragments(w.u, index, t, nt);
+        };
+        auto add_sum = [&](int x, const f32x4 (&from)[TT][NT]) {
+            const float f = decay_power(g, min(b.seg, pl.seq_len - number(x) * b.seg));
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) E[t][nt][r] = f * E[t][nt][r] + add[r];
-                }
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) E[t][nt][r] = f * E[t][nt][r] + from[t][nt][r];
+        };
+        for (int x = 0; x < before; x += 2) {
+            f32x4 U0[TT][NT], U1[TT][NT];
+            load_sum(x, U0);
+            if (x + 1 < before) load_sum(x + 1, U1);
+            add_sum(x, U0);
+            if (x + 1 < before) add_sum(x + 1, U1);
         }
     }
 
@@ -372,45 +413,83 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
     if constexpr (OUT) pa = view(w.a);
     pb = view(w.b);
     pc = view(w.c);
-    TileA ta, tb;
+    const int sa = (int)w.a.tok, sb = (int)w.b.tok, sc = (int)w.c.tok;
+    // (row strides of a chunk fit 32 bits; a reversed chunk's rows lie at n-1-r)
+    const int rsgn = w.reverse ? -1 : 1;
+    const int fa = TileA::first(rsgn * sa, 0, w.Da), fb = TileB::first(rsgn * sb, 0, w.Da);
+    const int fc = TileC::first(rsgn * sc, slice * COLS, w.Dc);
+    TileA ta;
+    TileB tb;
     TileC tc;
     auto fetch = [&](int x) {
         const int ci = w.reverse ? chunks - 1 - x : x;
         const int n = min(CH, pl.len - ci * CH);
-        const int64_t row = ci * CH + (w.reverse ? n - 1 : 0);
-        const int sgn = w.reverse ? -1 : 1;
-        if constexpr (OUT) ta.load(pa + row * w.a.tok, sgn * w.a.tok, n, 0, w.Da);
-        tb.load(pb + row * w.b.tok, sgn * w.b.tok, n, 0, w.Da);
-        tc.load(pc + row * w.c.tok, sgn * w.c.tok, n, slice * COLS, w.Dc);
+        const int64_t row = ci * CH;
+        if constexpr (OUT) ta.load(pa + row * w.a.tok, sa, fa, n, w.Da * T::bytes, w.reverse);
+        tb.load(pb + row * w.b.tok, sb, fb, n, w.Da * T::bytes, w.reverse);
+        tc.load(pc + row * w.c.tok, sc, fc, n, w.Dc * T::bytes, w.reverse);
     };
-    const float pscale = w.oscale * w.uscale;
+    // the wavefront's pair tiles
+    constexpr int PT = CI == 4 ? 3 : 1;
+    int tile_i[PT], tile_j[PT];
+    if constexpr (CI == 4) {
+        tile_i[0] = wv < 2 ? 3 : 2, tile_j[0] = 2 * (wv & 1);                            // 3,0 3,2 2,0 2,2
+        tile_i[1] = wv < 2 ? 3 : 4 - wv, tile_j[1] = wv == 0 ? 1 : wv == 1 ? 3 : 3 - wv;  // 3,1 3,3 2,1 1,0
+        tile_i[PT - 1] = wv < 2 ? wv : 2, tile_j[PT - 1] = wv < 2 ? wv : 2 * (wv & 1);    // 0,0 1,1 again
+    } else {
+        static_assert(CI == 2, "chunks of 32 or 64 tokens");
+        tile_i[0] = wv == 0 ? 0 : 1, tile_j[0] = wv == 2 ? 1 : 0;  // 0,0 1,0 1,1 and 1,0 again
+    }
+    // lambda^(i-j) of a lane's elements of a tile on the diagonal and of the one before it, with the scale; the
+    // tiles farther apart by a factor (all powers >= 0: none overflows)
+    f32x4 near0, near1;
+    {
+        const float pscale = w.oscale * w.uscale;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int d = lr - 4 * lg - r;
+            near0[r] = lam(max(d, 0)) * pscale;
+            near1[r] = lam(16 + d) * pscale;
+        }
+    }
+    const float lam16 = CI > 2 ? lam(16) : 1.f, lam32 = CI > 2 ? lam(32) : 1.f;
+    const int oes = w.out_f32 ? 4 : T::bytes;
+    const int fo = col0 + 4 * NT * lg < w.Dc ? rsgn * lr * (b.H * w.Dc * oes) + (col0 + 4 * NT * lg) * oes : kFar;
+    float wj[KT][T::depth / 4] = {};
     double dg = 0.0;
     if (chunks > 0) fetch(0);
     for (int x = 0; x < chunks; ++x) {
         const int ci = w.reverse ? chunks - 1 - x : x;
         const int n = min(CH, pl.len - ci * CH);
-        __syncthreads();  // the tiles of the chunk before are read
-        if constexpr (OUT) ta.template store<true>(sm.a);
-        tb.template store<true>(sm.b);
-        tc.template store<false>(sm.c);
+        // (barriers of the loop wait for LDS only: the next chunk's loads and this one's stores stay in flight)
+        mx::barrier_lds();  // the tiles of the chunk before are read
+        if constexpr (OUT) ta.store(sm.a);
+        tb.store(sm.b);
+        tc.store(sm.c);
         if (x + 1 < chunks) fetch(x + 1);
-        __syncthreads();
+        mx::barrier_lds();
 
         if constexpr (OUT) {
-            // pair tiles (I, J), J <= I, transposed (rows: tokens j, columns: tokens i)
-            for (int t = wv; t < CI * (CI + 1) / 2; t += 4) {
-                const int I = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, J = t - I * (I + 1) / 2;
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            // the wavefront's pair tiles (I, J), J <= I, transposed (rows: tokens j, columns: tokens i), side by
+            // side; a wavefront with fewer takes its first one twice
+            f32x4 acc[PT];
 #pragma unroll
-                for (int kb = 0; kb < KD; ++kb)
-                    acc = mul_add(row_frag<BF16>(sm.b, LDA, 16 * J + lr, kb, lg),
-                                  row_frag<BF16>(sm.a, LDA, 16 * I + lr, kb, lg), acc);
+            for (int q = 0; q < PT; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < KD; ++kb)
+#pragma unroll
+                for (int q = 0; q < PT; ++q)
+                    acc[q] = mul_add(row_frag<BF16, kBoth>(sm.b, LDB, 16 * tile_j[q] + lr, kb, lg),
+                                     row_frag<BF16, kRows>(sm.a, LDA, 16 * tile_i[q] + lr, kb, lg), acc[q]);
+#pragma unroll
+            for (int q = 0; q < PT; ++q) {
+                const int I = tile_i[q], J = tile_j[q], apart = I - J;
                 f32x4 val, wgt;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int d = 16 * (I - J) + lr - 4 * lg - r;
-                    val[r] = d >= 0 ? acc[r] * (lam(max(d, 0)) * pscale) : 0.f;
-                    wgt[r] = val[r] * static_cast<float>(d);
+                    const float f = apart == 0 ? near0[r] : near1[r] * (apart == 1 ? 1.f : apart == 2 ? lam16 : lam32);
+                    val[r] = apart > 0 || lr >= 4 * lg + r ? acc[q][r] * f : 0.f;
+                    wgt[r] = val[r] * static_cast<float>(16 * apart + lr - 4 * lg - r);
                 }
                 if constexpr (BF16) {
                     const int at = ((I * KT + (J >> 1)) * 64 + lane) * 16 + (J & 1) * 8;
@@ -449,7 +528,7 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
                 }
 #pragma unroll
                 for (int I = 0; I < CI; ++I) {
-                    const frag af = row_frag<BF16>(sm.a, LDA, 16 * I + lr, kb, lg);
+                    const frag af = row_frag<BF16, kRows>(sm.a, LDA, 16 * I + lr, kb, lg);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         O[I][nt] = mul_add(hi[nt], af, O[I][nt]);
@@ -465,7 +544,6 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) O[I][nt][r] *= f;
             }
-            __syncthreads();  // the pair matrix is written
         }
 
         const bool end = last_seg && x + 1 == chunks;       // nothing reads E after it but the caller
@@ -533,12 +611,62 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
                 dg += static_cast<double>(sum);
             }
         }
+        // (c is read twice, here and behind the barrier: kept, it would not fit the registers)
+        auto c_frags = [&](int kb, frag (&to)[NT]) {
 #pragma unroll
-        for (int kb = 0; kb < KT; ++kb) {
-            frag cf[NT], wh[NT], wl[NT];
+            for (int nt = 0; nt < NT; ++nt) to[nt] = col_frag<BF16>(sm.c, LDC, wv * 16 * NT + 16 * nt, kb, lr, lg);
+        };
+        if (update) {
+            if (x < 2 || n < CH || less) {  // else as in the chunk before
+                // token j's write still decays n - less - j times
+                const float *wt = sm.rpow + (CH - n + less);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) cf[nt] = c_frag<BF16, NT>(sm.c, LDC, wv * 16 * NT, nt, kb, lr, lg);
-            if constexpr (OUT) {
+                for (int kb = 0; kb < KT; ++kb)
+#pragma unroll
+                    for (int e = 0; e < T::depth / 4; ++e) {
+                        const int j = T::depth * kb + (BF16 ? mx::kperm(lg, e) : 4 * lg + e);
+                        wj[kb][e] = j < n ? wt[j] * w.uscale : 0.f;
+                    }
+            }
+#pragma unroll
+            for (int kb = 0; kb < KT; ++kb) {
+                frag cf[NT], wh[NT], wm[NT], wl[NT];
+                c_frags(kb, cf);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (BF16) {
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = static_cast<float>(cf[nt][e]) * wj[kb][e];
+                        split8x3(y, wh[nt], wm[nt], wl[nt]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) wh[nt][e] = cf[nt][e] * wj[kb][e];
+                    }
+                }
+                frag bt = col_frag<BF16>(sm.b, LDB, 0, kb, lr, lg);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    const frag now = bt;
+                    if (t + 1 < TT) bt = col_frag<BF16>(sm.b, LDB, 16 * (t + 1), kb, lr, lg);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) E[t][nt] = mul_add(now, wh[nt], E[t][nt]);
+                    if constexpr (BF16) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) E[t][nt] = mul_add(now, wm[nt], E[t][nt]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) E[t][nt] = mul_add(now, wl[nt], E[t][nt]);
+                    }
+                }
+            }
+        }
+
+        if constexpr (OUT) {
+            mx::barrier_lds();  // the pair matrix is written
+#pragma unroll
+            for (int kb = 0; kb < KT; ++kb) {
+                frag cf[NT];
+                c_frags(kb, cf);
 #pragma unroll
                 for (int I = 0; I < CI; ++I) {
                     if (BF16 ? kb <= (I >> 1) : kb <= I) {
@@ -561,74 +689,46 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
                     }
                 }
             }
-            if (update) {
-                // token j's write still decays n - less - j times
-                const float *wt = sm.rpow + (CH - n + less);
-                float wj[T::depth / 4];
-#pragma unroll
-                for (int e = 0; e < T::depth / 4; ++e) {
-                    const int j = T::depth * kb + (BF16 ? mx::kperm(lg, e) : 4 * lg + e);
-                    wj[e] = wt[j] * w.uscale;
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (BF16) {
-                        float y[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = static_cast<float>(cf[nt][e]) * wj[e];
-                        mx::split8(y, wh[nt], wl[nt]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) wh[nt][e] = cf[nt][e] * wj[e];
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    const frag bt = col_frag<BF16>(sm.b, LDA, t, kb, lr, lg);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        E[t][nt] = mul_add(bt, wh[nt], E[t][nt]);
-                        if constexpr (BF16) E[t][nt] = mul_add(bt, wl[nt], E[t][nt]);
-                    }
-                }
-            }
-        }
-
-        if constexpr (OUT) {
+            // rows of the chunk: offsets as in Tile::load, stores past the bounds are dropped
             const int64_t row0 = (int64_t)(b.cu ? 0 : (int64_t)pl.n * b.T) + tok + ci * CH;
+            const int orow = b.H * w.Dc * oes;
+            const auto ro = __builtin_amdgcn_make_buffer_rsrc(w.out + (row0 * b.H + h) * w.Dc * oes, (short)0,
+                                                              (n - 1) * orow + w.Dc * oes, 0x00020000);
 #pragma unroll
             for (int I = 0; I < CI; ++I) {
-                const int i = 16 * I + lr, col = col0 + 4 * NT * lg;
-                if (i < n && col < w.Dc) {
-                    const int64_t at = ((row0 + (w.reverse ? n - 1 - i : i)) * b.H + h) * w.Dc + col;
-                    if (!BF16 || w.out_f32) {
+                const uint32_t off = w.reverse ? (uint32_t)fo + (uint32_t)((n - 1 - 16 * I) * orow)
+                                               : (uint32_t)fo + (uint32_t)(16 * I * orow);
+                typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+                typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+                if (!BF16 || w.out_f32) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[I][nt]), ro,
+                                                               (int)(off + 16 * nt), 0, 0);
+                } else {
+                    uint32_t v[2 * NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const mx::bf16x2 x0 = {static_cast<__bf16>(O[I][nt][0]), static_cast<__bf16>(O[I][nt][1])};
+                        const mx::bf16x2 x1 = {static_cast<__bf16>(O[I][nt][2]), static_cast<__bf16>(O[I][nt][3])};
+                        v[2 * nt] = __builtin_bit_cast(uint32_t, x0);
+                        v[2 * nt + 1] = __builtin_bit_cast(uint32_t, x1);
+                    }
+                    if constexpr (NT == 2)
+                        __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[0], v[1], v[2], v[3]}, ro, (int)off, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, ro, (int)off, 0, 0);
+                }
+                if constexpr (DG) {
+                    const int i = 16 * I + lr, col = col0 + 4 * NT * lg;
+                    if (w.x.p && !w.reverse && i < n && col < w.Dc) {
+                        const char *px = view(w.x) + (int64_t)(ci * CH + i) * w.x.tok + (int64_t)col * T::bytes;
+                        float sum = 0.f;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(w.out) + at + 4 * nt) = O[I][nt];
-                    } else {
-                        uint32_t v[2 * NT];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const mx::bf16x2 x0 = {static_cast<__bf16>(O[I][nt][0]), static_cast<__bf16>(O[I][nt][1])};
-                            const mx::bf16x2 x1 = {static_cast<__bf16>(O[I][nt][2]), static_cast<__bf16>(O[I][nt][3])};
-                            v[2 * nt] = __builtin_bit_cast(uint32_t, x0);
-                            v[2 * nt + 1] = __builtin_bit_cast(uint32_t, x1);
-                        }
-                        if constexpr (NT == 2)
-                            *reinterpret_cast<uint4 *>(w.out + at * 2) = make_uint4(v[0], v[1], v[2], v[3]);
-                        else
-                            *reinterpret_cast<uint2 *>(w.out + at * 2) = make_uint2(v[0], v[1]);
-                    }
-                    if constexpr (DG) {
-                        if (w.x.p && !w.reverse) {
-                            const char *px = view(w.x) + (int64_t)(ci * CH + i) * w.x.tok + (int64_t)col * T::bytes;
-                            float sum = 0.f;
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) sum += load_in<BF16>(px, 4 * nt + r) * Y[I][nt][r];
-                            dg += static_cast<double>(sum);
-                        }
+                            for (int r = 0; r < 4; ++r) sum += load_in<BF16>(px, 4 * nt + r) * Y[I][nt][r];
+                        dg += static_cast<double>(sum);
                     }
                 }
             }
@@ -639,7 +739,21 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) *fragments(w.u, part, t, nt) = E[t][nt];
+            for (int nt = 0; nt < NT; ++nt) {
+                *fragments(w.u, part, t, nt) = E[t][nt];
+                if (w.u_t) {
+                    // element (row, col) as (col, row) of the other walk's fragments
+                    const int row = 16 * t + 4 * lg, col = col0 + mcol + 4 * nt;
+                    const int ws = row / COLS, ww = row % COLS / (16 * NT), cc = row % (16 * NT);
+                    float *to = w.u_t + (((size_t)u * b.H + h) * set.slices + ws) * (size_t)(PAD * COLS) +
+                                ((((size_t)ww * TT + (col >> 4)) * NT + (cc >> 2) % NT) * 64 + (col >> 2 & 3) * 16 +
+                                 4 * (cc / (4 * NT))) * 4 + (col & 3);
+                    if (row < w.Da && col < w.Dc) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) to[4 * r] = E[t][nt][r];
+                    }
+                }
+            }
     } else {
         if (w.ef && last_seg) {
             // an empty sequence keeps its state: E holds e0, decayed in the forward direction

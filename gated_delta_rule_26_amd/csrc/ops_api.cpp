@@ -46,6 +46,8 @@ int check_desc(const gdr_head_decay_desc *d, bool step) {
     if (d->H > 0 && (d->Hk == 0 || d->H % d->Hk != 0)) return GDR_E_SHAPE;
     if (d->Dk < 8 || d->Dk > gdr::hd::kMaxWidth || d->Dk % 8 || d->Dv < 8 || d->Dv > gdr::hd::kMaxWidth || d->Dv % 8)
         return GDR_E_UNSUPPORTED;
+    // the outputs' rows of a chunk are addressed with 32-bit byte offsets
+    if (d->H > 16384) return GDR_E_SHAPE;
     const double tokens = (step ? 1.0 : (double)d->T) * (d->B > 0 ? d->B : 1);
     if (tokens * d->H * 256.0 > (double)kMost || (double)d->B * d->H * 65536.0 > (double)kMost) return GDR_E_SHAPE;
     return GDR_OK;
@@ -57,6 +59,8 @@ int check_view(const void *p, const int64_t *stride, int B, int T, int heads, in
     if (!p) return GDR_E_NULL;
     if (!aligned(p, 16)) return GDR_E_ALIGN;
     const int size[3] = {B, T, heads};
+    // the rows of a chunk (64 tokens) are addressed with 32-bit byte offsets
+    if (T > 1 && stride[1] > (int64_t)(1 << 24) / es) return GDR_E_SHAPE;
     int64_t far = width, step[3];
     for (int i = 0; i < 3; ++i) {
         step[i] = size[i] > 1 ? stride[i] : 0;  // a stride that is not taken does not matter
@@ -306,6 +310,7 @@ int gdr_head_decay_bwd(const gdr_head_decay_desc *d, const int32_t *cu, const vo
     wk.out_f32 = shared;
     wk.e0 = ds_final; wk.e0_t = 1;
     wk.u = at(s.sums + 2 * sums);
+    wv.u_t = wk.u;  // dv's and dk's states are transposes of each other: summed once
     wq.zero_outside = wv.zero_outside = wk.zero_outside = 1;
     const size_t groups = (size_t)p.b.units * d->H * p.slices;
     if (dg) {
@@ -320,11 +325,12 @@ int gdr_head_decay_bwd(const gdr_head_decay_desc *d, const int32_t *cu, const vo
     set.b.cu = cu;
     set.b.g = g;
     set.slices = p.slices;
-    set.count = 3;
+    set.count = 2;
     set.w[0] = wq;
     set.w[1] = wv;
     set.w[2] = wk;
     if (p.sums && (rc = hip_status(gdr::hd::launch_segment_sums(set, bf16, p.sh, st))) != GDR_OK) return rc;
+    set.count = 3;
     if (dg) {
         // dk's walk reads the states that dq's keeps
         set.count = 1;

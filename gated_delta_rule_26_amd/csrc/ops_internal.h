@@ -40,6 +40,7 @@ struct Walk {
     int e0_decay = 0;           // E starts from lambda e0 (forward) or e0 (reversed)
     float *ef = nullptr;        // [N, H, Da, Dc] the last state: S of the forward pass, ds0 of a reversed one
     float *u = nullptr;         // segment sums, fragment order
+    float *u_t = nullptr;       // and transposed, for the walk with the widths exchanged
     // dL/dg: x holds the tensor that `out` is the gradient of; chunk_e the E of every chunk, fragment order
     View x;
     float *chunk_e = nullptr;

@@ -18,10 +18,10 @@
  * Layouts of this family:
  *  - q [.., H, Dk], k [.., Hk, Dk], v [.., Hk, Dv] and d_o [.., H, Dv] may be
  *    strided: the last dimension is contiguous, the others have the strides of
- *    the descriptor (in elements, >= 0; 0 repeats a row), with every row
- *    16-byte aligned.  Views of one fused projection need no copy.
+ *    the descriptor (in elements, >= 0; 0 repeats a row; between tokens 16 MiB
+ *    at most), with every row 16-byte aligned.  Views of one fused projection need no copy.
  *  - Outputs and states are contiguous; dq, dk, dv have the inputs' type.
- *  - Hk divides H; Dk and Dv are multiples of 8 from 8 to 256.
+ *  - Hk divides H, H is at most 16384; Dk and Dv are multiples of 8 from 8 to 256.
  *  - Values are not checked: g should be <= 0.  A value of k, v or d_o that is not
  *    finite makes the other tokens of its chunk (64 tokens at most, also
  *    earlier ones) undefined, not only the later ones.

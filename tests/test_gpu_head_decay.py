@@ -245,6 +245,15 @@ def test_views_and_broadcasts():
     a = gdr.head_decay_fwd(x["q"], k1, v1, x["g"])
     b = gdr.head_decay_fwd(x["q"], k1.contiguous(), v1.contiguous(), x["g"])
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # the same key at every token
+    k1 = x["k"][:, :1].expand(2, 90, 2, 64)
+    a = gdr.head_decay_bwd(x["q"], k1, x["v"], x["g"], x["d_o"])
+    b = gdr.head_decay_bwd(x["q"], k1.contiguous(), x["v"], x["g"], x["d_o"])
+    for n in ("dq", "dk", "dv", "dg", "ds0"):
+        assert torch.equal(a[n], b[n]), n
+    a = gdr.head_decay_fwd(x["q"], k1, x["v"], x["g"])
+    b = gdr.head_decay_fwd(x["q"], k1.contiguous(), x["v"], x["g"])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_equal_calls_give_equal_bits():
