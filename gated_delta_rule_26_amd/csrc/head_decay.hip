@@ -38,8 +38,8 @@ constexpr int kFar = 0x60000000;  // a byte offset out of any chunk's range, ste
 
 __device__ __forceinline__ float decay_power(float g, int x) { return x == 0 ? 1.f : expf(static_cast<float>(x) * g); }
 
-// Inclusive scan over the workgroup's 256 threads; `tmp` holds 4 values.  Two barriers.
-template <bool MAX>
+// Inclusive scan over the workgroup's WV wavefronts; `tmp` holds WV values.  Two barriers.
+template <bool MAX, int WV>
 __device__ int block_scan(int x, int *tmp) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
@@ -51,7 +51,7 @@ __device__ int block_scan(int x, int *tmp) {
     if (lane == 63) tmp[w] = x;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < WV - 1; ++i)
         if (i < w) x = MAX ? max(x, tmp[i]) : x + tmp[i];
     return x;
 }
@@ -65,11 +65,11 @@ struct Place {
 };
 
 struct PlaceSmem {
-    int tmp[4];
+    int tmp[8];
     int found[6];
 };
 
-template <int CH, bool COUNT>
+template <int CH, bool COUNT, int WV>
 __device__ Place find_place(const Batch &b, int u, PlaceSmem &sm) {
     Place p;
     p.first = 0;
@@ -88,17 +88,17 @@ __device__ Place find_place(const Batch &b, int u, PlaceSmem &sm) {
         if (t == 0) sm.found[0] = -1;
         int top = 0, units = 0, chunks = 0;
         p.first = min(max(b.cu[0], 0), b.T);
-        for (int base = 0; base < b.N; base += kThreads) {
+        for (int base = 0; base < b.N; base += 64 * WV) {
             const int i = base + t;
             const int lo = i <= b.N ? min(max(b.cu[i], 0), b.T) : 0;
             const int hi = i < b.N ? min(max(b.cu[i + 1], 0), b.T) : 0;
-            const int start = max(top, block_scan<true>(lo, sm.tmp));
+            const int start = max(top, block_scan<true, WV>(lo, sm.tmp));
             const int end = max(start, hi);
             const int mine = i < b.N ? max(1, (end - start + b.seg - 1) / b.seg) : 0;
-            const int upto = units + block_scan<false>(mine, sm.tmp);
+            const int upto = units + block_scan<false, WV>(mine, sm.tmp);
             const int own = i < b.N ? (end - start + CH - 1) / CH : 0;
             int chunks_to = 0;
-            if constexpr (COUNT) chunks_to = chunks + block_scan<false>(own, sm.tmp);
+            if constexpr (COUNT) chunks_to = chunks + block_scan<false, WV>(own, sm.tmp);
             if (i < b.N && u >= upto - mine && u < upto) {
                 sm.found[0] = i;
                 sm.found[1] = start;
@@ -108,7 +108,7 @@ __device__ Place find_place(const Batch &b, int u, PlaceSmem &sm) {
                 sm.found[5] = chunks_to - own;
             }
             __syncthreads();  // the scans' last reads of tmp are done
-            if (t == kThreads - 1) {
+            if (t == 64 * WV - 1) {
                 sm.tmp[0] = max(start, end);
                 sm.tmp[1] = upto;
                 sm.tmp[2] = chunks_to;
@@ -169,15 +169,15 @@ __device__ __forceinline__ f32x4 mul_add(f32x4 a, f32x4 b, f32x4 c) {
 // transposing read's half lie side by side.)
 enum Order { kRows, kBoth, kColumns };
 
-template <bool BF16, int W, int ROWS, Order ORD, int NT = 1>
+template <bool BF16, int W, int ROWS, Order ORD, int NT, int WV>
 struct Tile {
     using T = El<BF16>;
     static constexpr int per = 16 / T::bytes;       // elements of a piece
     static constexpr int pieces = W / per;          // of a row
-    static constexpr int rpp = kThreads / pieces;   // rows of a pass
+    static constexpr int rpp = 64 * WV / pieces;    // rows of a pass
     static constexpr int passes = ROWS / rpp;
     static constexpr int ld = W + (BF16 ? (ORD == kRows ? 8 : 16) : 4);
-    static_assert(kThreads % pieces == 0 && ROWS % rpp == 0, "tile must divide among the threads");
+    static_assert(64 * WV % pieces == 0 && ROWS % rpp == 0, "tile must divide among the threads");
     uint4 r[passes];
 
     // This thread's first byte of a chunk of `stride` bytes a row, out of any chunk's range where the channel
@@ -254,49 +254,84 @@ __device__ __forceinline__ typename El<BF16>::frag col_frag(const typename El<BF
     }
 }
 
-// Eight fp32 values as three bf16 terms, 24 bits: x = hi + mid + lo to fp32's own rounding.
-__device__ __forceinline__ void split8x3(const float *x, bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
-    float rest[8];
-    hi = bf16x8{static_cast<__bf16>(x[0]), static_cast<__bf16>(x[1]), static_cast<__bf16>(x[2]),
-                static_cast<__bf16>(x[3]), static_cast<__bf16>(x[4]), static_cast<__bf16>(x[5]),
-                static_cast<__bf16>(x[6]), static_cast<__bf16>(x[7])};
+// Two fp32 values rounded to bf16, packed; as two terms (x = hi + lo to 2^-17) and what hi leaves.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack2(float x0, float x1) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x0, x1}), mx::bf16x2));
+}
+__device__ __forceinline__ void rest2(float &x0, float &x1, uint32_t hi) {
+    x0 -= __uint_as_float(hi << 16);
+    x1 -= __uint_as_float(hi & 0xffff0000u);
+}
+// Two stacked tiles of an accumulator as a fragment in two terms.
+__device__ __forceinline__ void split_tiles(f32x4 t0, f32x4 t1, bf16x8 &hi, bf16x8 &lo) {
+    float x[8] = {t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]};
+    uint32_t h[4], l[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) rest[e] = x[e] - static_cast<float>(hi[e]);
-    mx::split8(rest, mid, lo);
+    for (int e = 0; e < 4; ++e) {
+        h[e] = pack2(x[2 * e], x[2 * e + 1]);
+        rest2(x[2 * e], x[2 * e + 1], h[e]);
+        l[e] = pack2(x[2 * e], x[2 * e + 1]);
+    }
+    hi = __builtin_bit_cast(bf16x8, make_uint4(h[0], h[1], h[2], h[3]));
+    lo = __builtin_bit_cast(bf16x8, make_uint4(l[0], l[1], l[2], l[3]));
+}
+// Eight fp32 values as three bf16 terms, 24 bits: x = hi + mid + lo to fp32's own rounding.
+__device__ __forceinline__ void split8x3(float *x, bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
+    uint32_t h[4], m[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = pack2(x[2 * e], x[2 * e + 1]);
+        rest2(x[2 * e], x[2 * e + 1], h[e]);
+        m[e] = pack2(x[2 * e], x[2 * e + 1]);
+        rest2(x[2 * e], x[2 * e + 1], m[e]);
+        l[e] = pack2(x[2 * e], x[2 * e + 1]);
+    }
+    hi = __builtin_bit_cast(bf16x8, make_uint4(h[0], h[1], h[2], h[3]));
+    mid = __builtin_bit_cast(bf16x8, make_uint4(m[0], m[1], m[2], m[3]));
+    lo = __builtin_bit_cast(bf16x8, make_uint4(l[0], l[1], l[2], l[3]));
+}
+
+// The pair matrix's fragment of token tile I, token block kb (bf16: kb <= I / 2; fp32: kb <= I).
+template <bool BF16, int CI>
+__device__ __forceinline__ int pair_frag(int I, int kb) {
+    if constexpr (BF16) return CI == 2 ? I : mx::lower_frag(I, kb);
+    else return I * CI + kb;
 }
 
 enum { kSums = 0, kWalk = 1, kWalkDg = 2 };
 
-template <bool BF16, int PAD, int NT, int CH, int MODE>
+template <bool BF16, int PAD, int NT, int CH, int WV, int MODE>
 struct Smem {
     using L = typename El<BF16>::lds;
-    static constexpr int nfrag = BF16 ? (CH / 16) * (CH / 32) : (CH / 16) * (CH / 16);
-    __align__(16) L a[MODE == kSums ? 1 : CH * Tile<BF16, PAD, CH, kRows>::ld];
-    __align__(16) L b[CH * Tile<BF16, PAD, CH, kBoth>::ld];
-    __align__(16) L c[CH * Tile<BF16, 64 * NT, CH, kColumns, NT>::ld];
+    static constexpr int nfrag = BF16 ? (CH == 64 ? 6 : 2) : (CH / 16) * (CH / 16);
+    __align__(16) L a[MODE == kSums ? 1 : CH * Tile<BF16, PAD, CH, kRows, 1, WV>::ld];
+    __align__(16) L b[CH * Tile<BF16, PAD, CH, kBoth, 1, WV>::ld];
+    __align__(16) L c[CH * Tile<BF16, 16 * NT * WV, CH, kColumns, NT, WV>::ld];
     __align__(16) char p[MODE == kSums ? 16 : nfrag * 1024];
     __align__(16) char ph[MODE == kWalkDg ? nfrag * 1024 : 16];  // (i - j) times the pair matrix, hi
     __align__(16) char pl[MODE == kWalkDg ? nfrag * 1024 : 16];  // and lo
     __align__(16) float rpow[2 * CH + 8];                        // lambda^(CH - y), 0 behind
-    double dg[4];
+    __align__(16) float write[CH];                               // what token j's write is multiplied by
+    double dg[WV];
     PlaceSmem place;
 };
 
-template <bool BF16, int PAD, int NT, int CH, int MODE>
-__global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
+template <bool BF16, int PAD, int NT, int CH, int WV, int MODE>
+__global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void walk_kernel(WalkSet set) {
     using T = El<BF16>;
     using frag = typename T::frag;
     constexpr int KD = PAD / T::depth;   // channel blocks of a row
     constexpr int KT = CH / T::depth;    // token blocks of a chunk
     constexpr int CI = CH / 16;          // token tiles of a chunk
     constexpr int TT = PAD / 16;         // row tiles of the state
-    constexpr int COLS = 64 * NT;
+    constexpr int COLS = 16 * NT * WV;
     constexpr bool OUT = MODE != kSums, DG = MODE == kWalkDg;
-    using TileA = Tile<BF16, PAD, CH, kRows>;
-    using TileB = Tile<BF16, PAD, CH, kBoth>;
-    using TileC = Tile<BF16, COLS, CH, kColumns, NT>;
+    using TileA = Tile<BF16, PAD, CH, kRows, 1, WV>;
+    using TileB = Tile<BF16, PAD, CH, kBoth, 1, WV>;
+    using TileC = Tile<BF16, COLS, CH, kColumns, NT, WV>;
     constexpr int LDA = TileA::ld, LDB = TileB::ld, LDC = TileC::ld;
-    __shared__ Smem<BF16, PAD, NT, CH, MODE> sm;
+    __shared__ Smem<BF16, PAD, NT, CH, WV, MODE> sm;
 
     const Walk &w = set.w[blockIdx.y];
     const Batch &b = set.b;
@@ -305,14 +340,14 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
     int group, slice;
     mx::state_slot(blockIdx.x, b.units * b.H, set.slices, group, slice);
     const int u = group / b.H, h = group - u * b.H;
-    const Place pl = find_place<CH, DG>(b, u, sm.place);
+    const Place pl = find_place<CH, DG, WV>(b, u, sm.place);
     const size_t part = ((size_t)u * b.H + h) * set.slices + slice;  // of u, chunk_e, dg_part
     const int col0 = slice * COLS + wv * 16 * NT;                    // the wavefront's first column
     if (OUT && b.cu && w.zero_outside && u == 0) {
         const int es = w.out_f32 ? 4 : T::bytes, per = 16 / es;
         const int cols = min(COLS, w.Dc - slice * COLS);
         const int outside = pl.first + (b.T - pl.last);
-        for (int x = tid; x < outside * (cols / per); x += kThreads) {
+        for (int x = tid; x < outside * (cols / per); x += 64 * WV) {
             const int i = x / (cols / per), row = i < pl.first ? i : pl.last + (i - pl.first);
             char *dst = w.out + (((int64_t)row * b.H + h) * w.Dc + slice * COLS + (x % (cols / per)) * per) * es;
             *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
@@ -327,12 +362,12 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
     if (!OUT && last_seg) return;  // no segment starts from its sum
 
     const float g = b.g[h];
-    for (int y = tid; y < 2 * CH + 8; y += kThreads) sm.rpow[y] = y <= CH ? decay_power(g, CH - y) : 0.f;
+    for (int y = tid; y < 2 * CH + 8; y += 64 * WV) sm.rpow[y] = y <= CH ? decay_power(g, CH - y) : 0.f;
     auto lam = [&](int x) { return sm.rpow[CH - x]; };  // lambda^x, 0 <= x <= CH
     if constexpr (OUT && BF16) {
         // the upper tiles inside the fragments' 32-blocks stay zero
-        for (int x = tid; x < CI * KT * 64; x += kThreads) {
-            const int I = x / 64 / KT, kb = x / 64 % KT;
+        for (int x = tid; x < Smem<BF16, PAD, NT, CH, WV, MODE>::nfrag * 64; x += 64 * WV) {
+            const int I = CI == 2 ? x / 64 : mx::frag_M(x / 64), kb = CI == 2 ? 0 : mx::frag_kb(x / 64);
             if (2 * kb + 1 > I) {
                 *reinterpret_cast<uint4 *>(sm.p + x * 16) = make_uint4(0, 0, 0, 0);
                 if constexpr (DG) {
@@ -429,16 +464,15 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
         tb.load(pb + row * w.b.tok, sb, fb, n, w.Da * T::bytes, w.reverse);
         tc.load(pc + row * w.c.tok, sc, fc, n, w.Dc * T::bytes, w.reverse);
     };
-    // the wavefront's pair tiles
-    constexpr int PT = CI == 4 ? 3 : 1;
+    // The wavefront's pair tiles, PT side by side: four wavefronts have three at most of ten (one with two takes
+    // its first again), eight have one each and then the two last ones; of three, one each.
+    constexpr int PT = CI == 4 && WV == 4 ? 3 : 1;
+    const int pair_rounds = CI == 4 ? (WV == 8 && wv < 2 ? 2 : 1) : wv < 3 ? 1 : 0;
     int tile_i[PT], tile_j[PT];
-    if constexpr (CI == 4) {
+    if constexpr (PT == 3) {
         tile_i[0] = wv < 2 ? 3 : 2, tile_j[0] = 2 * (wv & 1);                            // 3,0 3,2 2,0 2,2
         tile_i[1] = wv < 2 ? 3 : 4 - wv, tile_j[1] = wv == 0 ? 1 : wv == 1 ? 3 : 3 - wv;  // 3,1 3,3 2,1 1,0
-        tile_i[PT - 1] = wv < 2 ? wv : 2, tile_j[PT - 1] = wv < 2 ? wv : 2 * (wv & 1);    // 0,0 1,1 again
-    } else {
-        static_assert(CI == 2, "chunks of 32 or 64 tokens");
-        tile_i[0] = wv == 0 ? 0 : 1, tile_j[0] = wv == 2 ? 1 : 0;  // 0,0 1,0 1,1 and 1,0 again
+        tile_i[2] = wv < 2 ? wv : 2, tile_j[2] = wv < 2 ? wv : 2 * (wv & 1);              // 0,0 1,1 again
     }
     // lambda^(i-j) of a lane's elements of a tile on the diagonal and of the one before it, with the scale; the
     // tiles farther apart by a factor (all powers >= 0: none overflows)
@@ -455,7 +489,6 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
     const float lam16 = CI > 2 ? lam(16) : 1.f, lam32 = CI > 2 ? lam(32) : 1.f;
     const int oes = w.out_f32 ? 4 : T::bytes;
     const int fo = col0 + 4 * NT * lg < w.Dc ? rsgn * lr * (b.H * w.Dc * oes) + (col0 + 4 * NT * lg) * oes : kFar;
-    float wj[KT][T::depth / 4] = {};
     double dg = 0.0;
     if (chunks > 0) fetch(0);
     for (int x = 0; x < chunks; ++x) {
@@ -466,12 +499,23 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
         if constexpr (OUT) ta.store(sm.a);
         tb.store(sm.b);
         tc.store(sm.c);
+        const bool end = last_seg && x + 1 == chunks;       // nothing reads E after it but the caller
+        const int less = end && !w.reverse && OUT ? 1 : 0;  // S, not lambda S
+        const bool update = !OUT || !end || w.ef;
+        // token j's write still decays n - less - j times
+        if ((x < 2 || n < CH || less) && tid < CH) sm.write[tid] = tid < n ? sm.rpow[CH - n + less + tid] * w.uscale : 0.f;
         if (x + 1 < chunks) fetch(x + 1);
         mx::barrier_lds();
 
         if constexpr (OUT) {
             // the wavefront's pair tiles (I, J), J <= I, transposed (rows: tokens j, columns: tokens i), side by
             // side; a wavefront with fewer takes its first one twice
+            for (int round = 0; round < pair_rounds; ++round) {
+            if constexpr (PT == 1) {
+                const int t = wv + 8 * round;
+                tile_i[0] = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0;
+                tile_j[0] = t - tile_i[0] * (tile_i[0] + 1) / 2;
+            }
             f32x4 acc[PT];
 #pragma unroll
             for (int q = 0; q < PT; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -492,10 +536,8 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
                     wgt[r] = val[r] * static_cast<float>(16 * apart + lr - 4 * lg - r);
                 }
                 if constexpr (BF16) {
-                    const int at = ((I * KT + (J >> 1)) * 64 + lane) * 16 + (J & 1) * 8;
-                    const bf16x4 v = {static_cast<__bf16>(val[0]), static_cast<__bf16>(val[1]),
-                                      static_cast<__bf16>(val[2]), static_cast<__bf16>(val[3])};
-                    *reinterpret_cast<bf16x4 *>(sm.p + at) = v;
+                    const int at = (pair_frag<BF16, CI>(I, J >> 1) * 64 + lane) * 16 + (J & 1) * 8;
+                    *reinterpret_cast<uint2 *>(sm.p + at) = make_uint2(pack2(val[0], val[1]), pack2(val[2], val[3]));
                     if constexpr (DG) {
                         uint2 hi, lo;
                         mx::split2(wgt[0], wgt[1], hi.x, lo.x);
@@ -504,10 +546,11 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
                         *reinterpret_cast<uint2 *>(sm.pl + at) = lo;
                     }
                 } else {
-                    const int at = ((I * CI + J) * 64 + lane) * 16;
+                    const int at = (pair_frag<BF16, CI>(I, J) * 64 + lane) * 16;
                     *reinterpret_cast<f32x4 *>(sm.p + at) = val;
                     if constexpr (DG) *reinterpret_cast<f32x4 *>(sm.ph + at) = wgt;
                 }
+            }
             }
         }
 
@@ -523,7 +566,7 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
                 frag hi[NT], lo[NT];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (BF16) mx::pair_split(E[2 * kb][nt], E[2 * kb + 1][nt], hi[nt], lo[nt]);
+                    if constexpr (BF16) split_tiles(E[2 * kb][nt], E[2 * kb + 1][nt], hi[nt], lo[nt]);
                     else hi[nt] = E[kb][nt];
                 }
 #pragma unroll
@@ -546,9 +589,6 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
             }
         }
 
-        const bool end = last_seg && x + 1 == chunks;       // nothing reads E after it but the caller
-        const int less = end && !w.reverse && OUT ? 1 : 0;  // S, not lambda S
-        const bool update = !OUT || !end || w.ef;
         if constexpr (DG) {
             if (w.chunk_e) {
                 const size_t index = ((size_t)(pl.chunk0 + ci) * b.H + h) * set.slices + slice;
@@ -617,31 +657,24 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
             for (int nt = 0; nt < NT; ++nt) to[nt] = col_frag<BF16>(sm.c, LDC, wv * 16 * NT + 16 * nt, kb, lr, lg);
         };
         if (update) {
-            if (x < 2 || n < CH || less) {  // else as in the chunk before
-                // token j's write still decays n - less - j times
-                const float *wt = sm.rpow + (CH - n + less);
-#pragma unroll
-                for (int kb = 0; kb < KT; ++kb)
-#pragma unroll
-                    for (int e = 0; e < T::depth / 4; ++e) {
-                        const int j = T::depth * kb + (BF16 ? mx::kperm(lg, e) : 4 * lg + e);
-                        wj[kb][e] = j < n ? wt[j] * w.uscale : 0.f;
-                    }
-            }
 #pragma unroll
             for (int kb = 0; kb < KT; ++kb) {
                 frag cf[NT], wh[NT], wm[NT], wl[NT];
                 c_frags(kb, cf);
+                f32x4 wj[T::depth / 16];
+#pragma unroll
+                for (int y = 0; y < T::depth / 16; ++y)
+                    wj[y] = *reinterpret_cast<const f32x4 *>(sm.write + T::depth * kb + 16 * y + 4 * lg);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     if constexpr (BF16) {
                         float y[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = static_cast<float>(cf[nt][e]) * wj[kb][e];
+                        for (int e = 0; e < 8; ++e) y[e] = static_cast<float>(cf[nt][e]) * wj[e / 4][e % 4];
                         split8x3(y, wh[nt], wm[nt], wl[nt]);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) wh[nt][e] = cf[nt][e] * wj[kb][e];
+                        for (int e = 0; e < 4; ++e) wh[nt][e] = cf[nt][e] * wj[0][e];
                     }
                 }
                 frag bt = col_frag<BF16>(sm.b, LDB, 0, kb, lr, lg);
@@ -670,7 +703,7 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
 #pragma unroll
                 for (int I = 0; I < CI; ++I) {
                     if (BF16 ? kb <= (I >> 1) : kb <= I) {
-                        const int at = ((I * KT + kb) * 64 + lane) * 16;
+                        const int at = (pair_frag<BF16, CI>(I, kb) * 64 + lane) * 16;
                         const frag pf = *reinterpret_cast<const frag *>(sm.p + at);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) O[I][nt] = mul_add(cf[nt], pf, O[I][nt]);
@@ -709,10 +742,8 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
                     uint32_t v[2 * NT];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const mx::bf16x2 x0 = {static_cast<__bf16>(O[I][nt][0]), static_cast<__bf16>(O[I][nt][1])};
-                        const mx::bf16x2 x1 = {static_cast<__bf16>(O[I][nt][2]), static_cast<__bf16>(O[I][nt][3])};
-                        v[2 * nt] = __builtin_bit_cast(uint32_t, x0);
-                        v[2 * nt + 1] = __builtin_bit_cast(uint32_t, x1);
+                        v[2 * nt] = pack2(O[I][nt][0], O[I][nt][1]);
+                        v[2 * nt + 1] = pack2(O[I][nt][2], O[I][nt][3]);
                     }
                     if constexpr (NT == 2)
                         __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[0], v[1], v[2], v[3]}, ro, (int)off, 0, 0);
@@ -779,29 +810,37 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(WalkSet set) {
                 if (lane == 0) sm.dg[wv] = dg;
                 __syncthreads();
                 if (tid == 0)
-                    w.dg_part[part] = (sm.dg[0] + sm.dg[1]) + (sm.dg[2] + sm.dg[3]);
+                    {
+                    double all = 0.0;
+                    for (int i = 0; i < WV; ++i) all += sm.dg[i];
+                    w.dg_part[part] = all;
+                }
             }
         }
     }
 }
 
-template <bool BF16, int PAD, int NT, int CH, int MODE>
+template <bool BF16, int PAD, int NT, int CH, int WV, int MODE>
 hipError_t launch(const WalkSet &s, hipStream_t stream) {
     const dim3 grid((unsigned)(s.b.units * s.b.H * s.slices), (unsigned)s.count);
-    hipLaunchKernelGGL((walk_kernel<BF16, PAD, NT, CH, MODE>), grid, dim3(kThreads), 0, stream, s);
+    hipLaunchKernelGGL((walk_kernel<BF16, PAD, NT, CH, WV, MODE>), grid, dim3(64 * WV), 0, stream, s);
     return hipGetLastError();
 }
 
 template <int MODE>
 hipError_t dispatch(const WalkSet &s, bool bf16, const Shape &sh, hipStream_t stream) {
     if (bf16) {
-        if (sh.pad == 64) return launch<true, 64, 1, 64, MODE>(s, stream);
-        if (sh.pad == 128) return launch<true, 128, 2, 64, MODE>(s, stream);
-        return launch<true, 256, 1, 32, MODE>(s, stream);
+        if (sh.pad == 64)
+            return sh.cols == 64 ? launch<true, 64, 1, 64, 4, MODE>(s, stream) : launch<true, 64, 1, 64, 8, MODE>(s, stream);
+        if (sh.pad == 128)
+            return sh.cols == 64 ? launch<true, 128, 1, 64, 4, MODE>(s, stream) : launch<true, 128, 1, 64, 8, MODE>(s, stream);
+        return launch<true, 256, 1, 32, 4, MODE>(s, stream);
     }
-    if (sh.pad == 64) return launch<false, 64, 1, 32, MODE>(s, stream);
-    if (sh.pad == 128) return launch<false, 128, 2, 32, MODE>(s, stream);
-    return launch<false, 256, 1, 32, MODE>(s, stream);
+    if (sh.pad == 64)
+        return sh.cols == 64 ? launch<false, 64, 1, 32, 4, MODE>(s, stream) : launch<false, 64, 1, 32, 8, MODE>(s, stream);
+    if (sh.pad == 128)
+        return sh.cols == 64 ? launch<false, 128, 1, 32, 4, MODE>(s, stream) : launch<false, 128, 1, 32, 8, MODE>(s, stream);
+    return launch<false, 256, 1, 32, 4, MODE>(s, stream);
 }
 
 // ---- sums over the query heads of a group, and of dL/dg's parts
@@ -842,10 +881,10 @@ __global__ __launch_bounds__(kThreads) void dg_sum_kernel(const double *__restri
 
 }  // namespace
 
-Shape shape_of(bool bf16, int wide) {
-    if (wide <= 64) return Shape{64, bf16 ? 64 : 32, 64};
-    if (wide <= 128) return Shape{128, bf16 ? 64 : 32, 128};
-    return Shape{256, 32, 64};
+Shape shape_of(bool bf16, int wide, int cols) {
+    const int chunk = bf16 && wide <= 128 ? 64 : 32;
+    if (wide <= 128) return Shape{wide <= 64 ? 64 : 128, chunk, cols <= 64 ? 64 : 128};
+    return Shape{256, chunk, 64};
 }
 size_t frag_bytes(const Shape &s, int slices) { return (size_t)s.pad * s.cols * slices * sizeof(float); }
 

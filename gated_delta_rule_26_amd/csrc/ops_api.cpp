@@ -91,7 +91,7 @@ struct Plan {
 };
 
 int make_plan(const gdr_head_decay_desc *d, bool packed, int wide, int cols, int walks, Plan *p) {
-    p->sh = gdr::hd::shape_of(d->dtype == GDR_BF16, wide);
+    p->sh = gdr::hd::shape_of(d->dtype == GDR_BF16, wide, cols);
     p->slices = (cols + p->sh.cols - 1) / p->sh.cols;
     const int64_t T = d->T, tokens = packed ? T : T * d->B;
     int64_t seg = tokens * d->H * p->slices * walks / 512;

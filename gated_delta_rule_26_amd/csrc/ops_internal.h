@@ -65,11 +65,11 @@ struct WalkSet {
     int slices = 0;  // column slices of a walk (the widest of them)
 };
 
-// Tile shape for widths up to `wide`: padded row width, chunk, columns of a slice.
+// Tile shape for rows up to `wide` and `cols` columns of the state: padded row width, chunk, columns of a slice.
 struct Shape {
     int pad, chunk, cols;
 };
-Shape shape_of(bool bf16, int wide);
+Shape shape_of(bool bf16, int wide, int cols);
 // Bytes of one E in fragment order, over all slices.
 size_t frag_bytes(const Shape &s, int slices);
 
