@@ -16,10 +16,11 @@ are: the last dimension contiguous, every row 16-byte aligned.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from . import F32, BF16, GdrError, _check_dev, _ptr, _stream, _used_on, load_library
+from . import F32, BF16, GdrError, _used_on, load_library
 
 __all__ = ["head_decay_fwd", "head_decay_fwd_varlen", "head_decay_bwd", "head_decay_bwd_varlen", "head_decay_step",
            "head_decay_fwd_workspace_size", "head_decay_bwd_workspace_size", "beam_select",
@@ -59,30 +60,49 @@ def _device(q):
     return q.device
 
 
-def _check_view(name, t, device, dtype, shape):
-    """A tensor that may be strided, but for its last dimension."""
+def _check_any(name, t, device, dtype, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel() > 0:
+
+
+def _check_view(name, t, device, dtype, shape):
+    """A tensor that may be strided, but for its last dimension."""
+    _check_any(name, t, device, dtype, shape)
+    if t.stride(-1) != 1 and shape[-1] > 1 and t.numel() > 0:
         raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _check_dev(name, t, device, dtype=None, shape=None):
+    _check_any(name, t, device, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+# the handle of torch's current stream, without the Stream object around it where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _strides(t, dims):
     """(sequence, token, head) strides of a tensor of which ``dims`` are there."""
     st = t.stride()
-    return {3: (st[0], st[1], st[2]), 2: (0, st[0], st[1]), 1: (st[0], 0, st[1])}[dims]
+    return st[:3] if dims == 3 else (0, st[0], st[1]) if dims == 2 else (st[0], 0, st[1])
 
 
 def _call(dev, name, *args):
     """The library call, on the tensors' device."""
     fn = getattr(load_library(), name)
-    if dev.index is None or dev.index == torch.cuda.current_device():
+    if dev.index == torch.cuda.current_device():
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -91,11 +111,15 @@ def _call(dev, name, *args):
         raise GdrError(rc, name)
 
 
-def _on(stream, dev):
-    st = _stream(stream, dev)
-    if st.device != dev:
-        raise ValueError(f"the stream is on {st.device}, the tensors on {dev}")
-    return st
+def _on(stream, dev, fresh):
+    """The handle of the stream the work is enqueued on: ``stream``, or torch's current stream of ``dev``.
+    ``fresh``: tensors allocated here, on the current stream."""
+    if stream is None:
+        return _raw_stream(dev.index)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    _used_on(stream, dev, *fresh)
+    return stream.cuda_stream
 
 
 def _workspace(workspace, need, dev, fresh):
@@ -123,6 +147,20 @@ def head_decay_fwd_workspace_size(desc: HeadDecayDesc, packed: bool = False) -> 
 
 def head_decay_bwd_workspace_size(desc: HeadDecayDesc, packed: bool = False, need_dg: bool = True) -> int:
     return _size("gdr_head_decay_bwd_workspace_size", ctypes.byref(desc), int(packed), int(need_dg))
+
+
+@functools.lru_cache(maxsize=1024)
+def _described(kind, need_dg, B, T, H, Hk, Dk, Dv, dtype, scale, *strides):
+    """(descriptor, workspace bytes) of a call: both follow from sizes and strides alone, and a program's calls
+    repeat them.  kind: "fwd", "bwd" (a second letter p: packed) or "step"."""
+    desc = make_head_decay_desc(B, T, H, Hk, Dk, Dv, dtype=dtype, scale=scale, q_stride=strides[0],
+                                k_stride=strides[1], v_stride=strides[2],
+                                do_stride=strides[3] if len(strides) > 3 else (0, 0, 0))
+    if kind == "step":
+        return desc, 0
+    if kind.startswith("fwd"):
+        return desc, head_decay_fwd_workspace_size(desc, kind == "fwdp")
+    return desc, head_decay_bwd_workspace_size(desc, kind == "bwdp", need_dg)
 
 
 def _tokens(q, k, v, g, cu_seqlens):
@@ -172,14 +210,13 @@ def _fwd(q, k, v, g, cu_seqlens, scale, s0, output_final_state, s_final, o, work
         s_final = torch.empty(state, dtype=torch.float32, device=dev)
         fresh.append(s_final)
     dims = 2 if packed else 3
-    desc = make_head_decay_desc(B, T, H, Hk, Dk, Dv, dtype=q.dtype, scale=scale, q_stride=_strides(q, dims),
-                                k_stride=_strides(k, dims), v_stride=_strides(v, dims))
-    workspace = _workspace(workspace, head_decay_fwd_workspace_size(desc, packed), dev, fresh)
-    st = _on(stream, dev)
-    _used_on(st, dev, *fresh)
+    desc, need = _described("fwdp" if packed else "fwd", False, B, T, H, Hk, Dk, Dv, q.dtype, float(scale),
+                            _strides(q, dims), _strides(k, dims), _strides(v, dims))
+    workspace = _workspace(workspace, need, dev, fresh)
+    st = _on(stream, dev, fresh)
     _call(dev, "gdr_head_decay_fwd", ctypes.byref(desc), _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
           _ptr(s0), _ptr(o), _ptr(s_final), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-          ctypes.c_void_p(st.cuda_stream))
+          st)
     return o, s_final
 
 
@@ -226,16 +263,14 @@ def _bwd(q, k, v, g, d_o, cu_seqlens, scale, s0, ds_final, need_dg, need_ds0, wo
             out[x].zero_()
     fresh = list(out.values())
     dims = 2 if packed else 3
-    desc = make_head_decay_desc(B, T, H, Hk, Dk, Dv, dtype=q.dtype, scale=scale, q_stride=_strides(q, dims),
-                                k_stride=_strides(k, dims), v_stride=_strides(v, dims),
-                                do_stride=_strides(d_o, dims))
-    workspace = _workspace(workspace, head_decay_bwd_workspace_size(desc, packed, need_dg), dev, fresh)
-    st = _on(stream, dev)
-    _used_on(st, dev, *fresh)
+    desc, need = _described("bwdp" if packed else "bwd", bool(need_dg), B, T, H, Hk, Dk, Dv, q.dtype, float(scale),
+                            _strides(q, dims), _strides(k, dims), _strides(v, dims), _strides(d_o, dims))
+    workspace = _workspace(workspace, need, dev, fresh)
+    st = _on(stream, dev, fresh)
     _call(dev, "gdr_head_decay_bwd", ctypes.byref(desc), _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
           _ptr(s0), _ptr(d_o), _ptr(ds_final), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]),
           _ptr(out["ds0"]), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-          ctypes.c_void_p(st.cuda_stream))
+          st)
     return out
 
 
@@ -302,15 +337,15 @@ def head_decay_step(q, k, v, g, state, *, scale: float = 1.0, slots=None, parent
         fresh.append(o)
     else:
         _check_dev("o", o, dev, q.dtype, (N, H, Dv))
-    desc = make_head_decay_desc(N, 1, H, Hk, Dk, Dv, dtype=q.dtype, scale=scale, q_stride=_strides(q, 1),
-                                k_stride=_strides(k, 1), v_stride=_strides(v, 1))
-    st = _on(stream, dev)
-    _used_on(st, dev, *fresh)
+    desc, _ = _described("step", False, N, 1, H, Hk, Dk, Dv, q.dtype, float(scale), _strides(q, 1), _strides(k, 1),
+                         _strides(v, 1))
+    st = _on(stream, dev, fresh)
     _call(dev, "gdr_head_decay_step", ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state),
-          state.shape[0], _ptr(slots), _ptr(parents), _ptr(state_out), _ptr(o), ctypes.c_void_p(st.cuda_stream))
+          state.shape[0], _ptr(slots), _ptr(parents), _ptr(state_out), _ptr(o), st)
     return o
 
 
+@functools.lru_cache(maxsize=1024)
 def beam_select_workspace_size(B: int, K: int, V: int) -> int:
     return _size("gdr_beam_select_workspace_size", B, K, V)
 
@@ -342,15 +377,14 @@ def beam_select(logits, scores, *, done=None, eos_token: int = -1, pad_token: in
     _check_dev("scores", scores, dev, torch.float32, (B, K))
     if done is not None:
         _check_dev("done", done, dev, torch.bool, (B, K))
-    fresh = [torch.empty((B, K), dtype=torch.float32, device=dev), torch.empty((B, K), dtype=torch.int32, device=dev),
-             torch.empty((B, K), dtype=torch.int32, device=dev), torch.empty((B, K), dtype=torch.bool, device=dev)]
-    out = tuple(fresh)
+    tokens = torch.empty_like(scores, dtype=torch.int32)
+    out = (torch.empty_like(scores), tokens, torch.empty_like(tokens), torch.empty_like(scores, dtype=torch.bool))
+    fresh = list(out)
     workspace = _workspace(workspace, beam_select_workspace_size(B, K, V), dev, fresh)
-    st = _on(stream, dev)
-    _used_on(st, dev, *fresh)
+    st = _on(stream, dev, fresh)
     _call(dev, "gdr_beam_select", B, K, V, _code(logits.dtype), _ptr(logits), row, _ptr(scores), _ptr(done),
           eos_token, pad_token, *(_ptr(x) for x in out), _ptr(workspace),
-          0 if workspace is None else workspace.numel(), ctypes.c_void_p(st.cuda_stream))
+          0 if workspace is None else workspace.numel(), st)
     return out
 
 
@@ -382,7 +416,7 @@ def beam_reorder(state, parents, *, dim: int = 0, out=None, stream=None):
         L *= x
     for x in state.shape[dim + 2:]:
         row *= x
-    st = _on(stream, dev)
+    st = _on(stream, dev, ())
     _call(dev, "gdr_beam_reorder", L, B, K, row, _ptr(state), _ptr(parents), _ptr(out),
-          ctypes.c_void_p(st.cuda_stream))
+          st)
     return out
