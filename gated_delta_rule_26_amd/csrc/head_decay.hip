@@ -379,6 +379,34 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     }
     __syncthreads();
 
+    // ---- the rows of the segment, and its first chunk's loads
+    const int chunks = (pl.len + CH - 1) / CH;
+    const char *pa = nullptr, *pb, *pc;
+    const int64_t tok = pl.tok0 + pl.t0;
+    auto view = [&](const View &v) { return v.p + (b.cu ? 0 : pl.n * v.seq) + (h / v.div) * v.head + tok * v.tok; };
+    if constexpr (OUT) pa = view(w.a);
+    pb = view(w.b);
+    pc = view(w.c);
+    const int sa = (int)w.a.tok, sb = (int)w.b.tok, sc = (int)w.c.tok;
+    // (row strides of a chunk fit 32 bits; a reversed chunk's rows lie at n-1-r)
+    const int rsgn = w.reverse ? -1 : 1;
+    const int fa = TileA::first(rsgn * sa, 0, w.Da), fb = TileB::first(rsgn * sb, 0, w.Da);
+    const int fc = TileC::first(rsgn * sc, slice * COLS, w.Dc);
+    TileA ta;
+    TileB tb;
+    TileC tc;
+    auto fetch = [&](int x) {
+        const int ci = w.reverse ? chunks - 1 - x : x;
+        const int n = min(CH, pl.len - ci * CH);
+        const int64_t row = ci * CH;
+        if constexpr (OUT) ta.load(pa + row * w.a.tok, sa, fa, n, w.Da * T::bytes, w.reverse);
+        tb.load(pb + row * w.b.tok, sb, fb, n, w.Da * T::bytes, w.reverse);
+        tc.load(pc + row * w.c.tok, sc, fc, n, w.Dc * T::bytes, w.reverse);
+    };
+    // (beside the state only where the registers hold both)
+    constexpr bool early = !(BF16 && PAD == 128 && WV == 8 && MODE == kWalk);
+    if (early && chunks > 0) fetch(0);
+
     // ---- the entering state
     const int mcol = 4 * NT * (lr >> 2) + (lr & 3);  // lane's column in tile 0 of the wavefront's columns
     const size_t e_base = ((size_t)pl.n * b.H + h) * w.Da * w.Dc;
@@ -441,31 +469,8 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     }
 
     // ---- the walk
-    const int chunks = (pl.len + CH - 1) / CH;
-    const char *pa = nullptr, *pb, *pc;
-    const int64_t tok = pl.tok0 + pl.t0;
-    auto view = [&](const View &v) { return v.p + (b.cu ? 0 : pl.n * v.seq) + (h / v.div) * v.head + tok * v.tok; };
-    if constexpr (OUT) pa = view(w.a);
-    pb = view(w.b);
-    pc = view(w.c);
-    const int sa = (int)w.a.tok, sb = (int)w.b.tok, sc = (int)w.c.tok;
-    // (row strides of a chunk fit 32 bits; a reversed chunk's rows lie at n-1-r)
-    const int rsgn = w.reverse ? -1 : 1;
-    const int fa = TileA::first(rsgn * sa, 0, w.Da), fb = TileB::first(rsgn * sb, 0, w.Da);
-    const int fc = TileC::first(rsgn * sc, slice * COLS, w.Dc);
-    TileA ta;
-    TileB tb;
-    TileC tc;
-    auto fetch = [&](int x) {
-        const int ci = w.reverse ? chunks - 1 - x : x;
-        const int n = min(CH, pl.len - ci * CH);
-        const int64_t row = ci * CH;
-        if constexpr (OUT) ta.load(pa + row * w.a.tok, sa, fa, n, w.Da * T::bytes, w.reverse);
-        tb.load(pb + row * w.b.tok, sb, fb, n, w.Da * T::bytes, w.reverse);
-        tc.load(pc + row * w.c.tok, sc, fc, n, w.Dc * T::bytes, w.reverse);
-    };
-    // The wavefront's pair tiles, PT side by side: four wavefronts have three at most of ten (one with two takes
-    // its first again), eight have one each and then the two last ones; of three, one each.
+    // The wavefront's pair tiles, PT side by side: four wavefronts have three of ten (one with two takes its first
+    // again), eight have one and then the two last ones, and of three tiles each has one.
     constexpr int PT = CI == 4 && WV == 4 ? 3 : 1;
     const int pair_rounds = CI == 4 ? (WV == 8 && wv < 2 ? 2 : 1) : wv < 3 ? 1 : 0;
     int tile_i[PT], tile_j[PT];
@@ -490,7 +495,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     const int oes = w.out_f32 ? 4 : T::bytes;
     const int fo = col0 + 4 * NT * lg < w.Dc ? rsgn * lr * (b.H * w.Dc * oes) + (col0 + 4 * NT * lg) * oes : kFar;
     double dg = 0.0;
-    if (chunks > 0) fetch(0);
+    if (!early && chunks > 0) fetch(0);
     for (int x = 0; x < chunks; ++x) {
         const int ci = w.reverse ? chunks - 1 - x : x;
         const int n = min(CH, pl.len - ci * CH);
@@ -508,14 +513,13 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
         mx::barrier_lds();
 
         if constexpr (OUT) {
-            // the wavefront's pair tiles (I, J), J <= I, transposed (rows: tokens j, columns: tokens i), side by
-            // side; a wavefront with fewer takes its first one twice
+            // pair tiles (I, J), J <= I, transposed (rows: tokens j, columns: tokens i)
             for (int round = 0; round < pair_rounds; ++round) {
-            if constexpr (PT == 1) {
-                const int t = wv + 8 * round;
-                tile_i[0] = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0;
-                tile_j[0] = t - tile_i[0] * (tile_i[0] + 1) / 2;
-            }
+                if constexpr (PT == 1) {
+                    const int t = wv + 8 * round;
+                    tile_i[0] = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0;
+                    tile_j[0] = t - tile_i[0] * (tile_i[0] + 1) / 2;
+                }
             f32x4 acc[PT];
 #pragma unroll
             for (int q = 0; q < PT; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -883,8 +887,9 @@ __global__ __launch_bounds__(kThreads) void dg_sum_kernel(const double *__restri
 
 Shape shape_of(bool bf16, int wide, int cols) {
     const int chunk = bf16 && wide <= 128 ? 64 : 32;
-    if (wide <= 128) return Shape{wide <= 64 ? 64 : 128, chunk, cols <= 64 ? 64 : 128};
-    return Shape{256, chunk, 64};
+    if (wide > 128) return Shape{256, chunk, 64, 2};
+    const bool both = cols > 64;  // eight wavefronts
+    return Shape{wide <= 64 ? 64 : 128, chunk, both ? 128 : 64, 2};
 }
 size_t frag_bytes(const Shape &s, int slices) { return (size_t)s.pad * s.cols * slices * sizeof(float); }
 

@@ -1,5 +1,6 @@
 // C ABI of the per-head-decay and beam-search operators: argument validation (host code, before any HIP
 // call), the plan of a call (tiles, segments, workspace) and its launches.  See include/gdr_ops.h.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -33,6 +34,8 @@ bool alias_free(const Range (&in)[NI], const Range (&out)[NO]) {
     }
     return true;
 }
+
+constexpr int kFill = 256;  // compute units
 
 constexpr size_t kMost = (size_t)1 << 46;  // elements of a tensor, and of a stride
 
@@ -79,9 +82,10 @@ int check_view(const void *p, const int64_t *stride, int B, int T, int heads, in
     return GDR_OK;
 }
 
-// How a call is cut up.  A workgroup walks a segment of a head and a column slice; segments are as long as
-// they can be with about two workgroups per compute unit (a segment costs a second reading of b and c, and
-// its sum), four chunks at least, and 32 of them per sequence at most (each starts from a chain of sums).
+// How a call is cut up.  A workgroup walks a segment of a head and a column slice.  A segment costs a second
+// reading of b and c and its sum, and all of them pay for a round of workgroups that is not full: so there are as
+// many segments as fill the card once (what is resident at a time), of 64 tokens at least, and kMaxSegments per
+// sequence at most (each starts from a chain of sums).
 struct Plan {
     Shape sh;
     int slices;
@@ -93,15 +97,18 @@ struct Plan {
 int make_plan(const gdr_head_decay_desc *d, bool packed, int wide, int cols, int walks, Plan *p) {
     p->sh = gdr::hd::shape_of(d->dtype == GDR_BF16, wide, cols);
     p->slices = (cols + p->sh.cols - 1) / p->sh.cols;
-    const int64_t T = d->T, tokens = packed ? T : T * d->B;
-    int64_t seg = tokens * d->H * p->slices * walks / 512;
-    if (seg < 256) seg = 256;
-    if (seg < (T + gdr::hd::kMaxSegments - 1) / gdr::hd::kMaxSegments)
-        seg = (T + gdr::hd::kMaxSegments - 1) / gdr::hd::kMaxSegments;
-    if (seg > T) seg = T > 0 ? T : 1;
-    int64_t per = T > 0 ? (T + seg - 1) / seg : 1;
-    if (!packed) seg = T > 0 ? (T + per - 1) / per : 1;  // equal parts
-    seg = (seg + 63) / 64 * 64;
+    const int64_t T = d->T;
+    const int64_t share = (int64_t)kFill * p->sh.resident / std::max<int64_t>((int64_t)d->H * p->slices * walks, 1);
+    int64_t seg, per = 1;
+    if (packed) {
+        // a sequence's last segment is half full on average
+        seg = T / std::max<int64_t>(share - d->B / 2, 1);
+        seg = std::max(seg, (T + gdr::hd::kMaxSegments - 1) / gdr::hd::kMaxSegments);
+    } else {
+        per = std::min<int64_t>(std::max<int64_t>(share / std::max(d->B, 1), 1), gdr::hd::kMaxSegments);
+        seg = (T + per - 1) / per;
+    }
+    seg = std::max<int64_t>((seg + 63) / 64 * 64, 64);
     per = T > 0 ? (T + seg - 1) / seg : 1;
     const int64_t units = packed ? T / seg + d->B : per * d->B;
     // one workgroup per (unit, head, slice): the grid must stay below 2^31
@@ -137,7 +144,7 @@ struct BwdSpace {
 };
 int plan_bwd(const gdr_head_decay_desc *d, bool packed, bool need_dg, Plan *p, BwdSpace *s) {
     const int wide = d->Dk > d->Dv ? d->Dk : d->Dv;
-    const int rc = make_plan(d, packed, wide, wide, 3, p);
+    const int rc = make_plan(d, packed, wide, wide, need_dg ? 2 : 3, p);
     if (rc != GDR_OK) return rc;
     const size_t tokens = packed ? (size_t)d->T : (size_t)d->T * d->B;
     const bool shared = d->H != d->Hk;

@@ -9,7 +9,7 @@ namespace hd {
 
 constexpr int kThreads = 256;
 constexpr int kMaxWidth = 256;
-constexpr int kMaxSegments = 32;  // of one sequence (fixed-length batch): the entering state is a chain over them
+constexpr int kMaxSegments = 64;  // of one sequence: the entering state is a chain over them
 
 // A strided [sequence, token, head, channel] tensor; strides in bytes.
 struct View {
@@ -65,9 +65,10 @@ struct WalkSet {
     int slices = 0;  // column slices of a walk (the widest of them)
 };
 
-// Tile shape for rows up to `wide` and `cols` columns of the state: padded row width, chunk, columns of a slice.
+// Tile shape for rows up to `wide` and `cols` columns of the state: padded row width, chunk, columns of a slice,
+// and the workgroups that a compute unit holds.
 struct Shape {
-    int pad, chunk, cols;
+    int pad, chunk, cols, resident;
 };
 Shape shape_of(bool bf16, int wide, int cols);
 // Bytes of one E in fragment order, over all slices.
