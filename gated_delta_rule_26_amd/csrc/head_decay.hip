@@ -494,6 +494,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     const float lam16 = CI > 2 ? lam(16) : 1.f, lam32 = CI > 2 ? lam(32) : 1.f;
     const int oes = w.out_f32 ? 4 : T::bytes;
     const int fo = col0 + 4 * NT * lg < w.Dc ? rsgn * lr * (b.H * w.Dc * oes) + (col0 + 4 * NT * lg) * oes : kFar;
+    const bool weighted = DG && w.x.p && !w.reverse;  // the walk that sums (i - j) times the pairs
     double dg = 0.0;
     if (!early && chunks > 0) fetch(0);
     for (int x = 0; x < chunks; ++x) {
@@ -542,7 +543,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
                 if constexpr (BF16) {
                     const int at = (pair_frag<BF16, CI>(I, J >> 1) * 64 + lane) * 16 + (J & 1) * 8;
                     *reinterpret_cast<uint2 *>(sm.p + at) = make_uint2(pack2(val[0], val[1]), pack2(val[2], val[3]));
-                    if constexpr (DG) {
+                    if (DG && weighted) {
                         uint2 hi, lo;
                         mx::split2(wgt[0], wgt[1], hi.x, lo.x);
                         mx::split2(wgt[2], wgt[3], hi.y, lo.y);
@@ -552,7 +553,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
                 } else {
                     const int at = (pair_frag<BF16, CI>(I, J) * 64 + lane) * 16;
                     *reinterpret_cast<f32x4 *>(sm.p + at) = val;
-                    if constexpr (DG) *reinterpret_cast<f32x4 *>(sm.ph + at) = wgt;
+                    if (DG && weighted) *reinterpret_cast<f32x4 *>(sm.ph + at) = wgt;
                 }
             }
             }
@@ -560,7 +561,9 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
 
         f32x4 O[CI][NT];
         if constexpr (OUT) {
-            // the state's read, transposed: rows c's channels, columns tokens
+            // the state's read, transposed: rows c's channels, columns tokens.  From here to the barrier a
+            // wavefront is mostly products: it goes first (the prefill walk's passes 122 -> 118 us)
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int I = 0; I < CI; ++I)
 #pragma unroll
@@ -699,6 +702,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
         }
 
         if constexpr (OUT) {
+            __builtin_amdgcn_s_setprio(0);
             mx::barrier_lds();  // the pair matrix is written
 #pragma unroll
             for (int kb = 0; kb < KT; ++kb) {
@@ -712,7 +716,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) O[I][nt] = mul_add(cf[nt], pf, O[I][nt]);
                         if constexpr (DG) {
-                            if (w.x.p && !w.reverse) {
+                            if (weighted) {
                                 const frag qh = *reinterpret_cast<const frag *>(sm.ph + at);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) Y[I][nt] = mul_add(cf[nt], qh, Y[I][nt]);
@@ -756,7 +760,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
                 }
                 if constexpr (DG) {
                     const int i = 16 * I + lr, col = col0 + 4 * NT * lg;
-                    if (w.x.p && !w.reverse && i < n && col < w.Dc) {
+                    if (weighted && i < n && col < w.Dc) {
                         const char *px = view(w.x) + (int64_t)(ci * CH + i) * w.x.tok + (int64_t)col * T::bytes;
                         float sum = 0.f;
 #pragma unroll
