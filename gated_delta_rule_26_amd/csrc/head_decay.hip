@@ -448,7 +448,11 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
 #pragma unroll
             for (int t = 0; t < TT; ++t)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) to[t][nt] = *fragments(w.u, index, t, nt);
+                for (int nt = 0; nt < NT; ++nt) {
+                    // (a transposed sum holds the state's own rows and columns only)
+                    to[t][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    if (16 * t + 4 * lg < w.Da && col0 + mcol + 4 * nt < w.Dc) to[t][nt] = *fragments(w.u, index, t, nt);
+                }
         };
         auto add_sum = [&](int x, const f32x4 (&from)[TT][NT]) {
             const float f = decay_power(g, min(b.seg, pl.seq_len - number(x) * b.seg));

@@ -24,7 +24,8 @@
  *  - Hk divides H, H is at most 16384; Dk and Dv are multiples of 8 from 8 to 256.
  *  - Values are not checked: g should be <= 0.  A value of k, v or d_o that is not
  *    finite makes the other tokens of its chunk (64 tokens at most, also
- *    earlier ones) undefined, not only the later ones.
+ *    earlier ones) undefined, not only the later ones;
+ *    so does a state that is not finite for all of its outputs.
  */
 #ifndef GDR_OPS_H
 #define GDR_OPS_H

@@ -45,6 +45,16 @@ def test_select(B, K, V, pad, dt):
     check(logits, scores, gdr.beam_select(logits, scores, done=done, eos_token=0, pad_token=V - 1), done, 0, V - 1)
 
 
+def test_select_workspace_used_again():
+    logits, scores = logits_of(4, 3, 5, 40001, torch.bfloat16, 3)
+    want = gdr.beam_select(logits, scores, eos_token=3)
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        for a, b in zip(gdr.beam_select(logits, scores, eos_token=3, workspace=ws), want):
+            assert torch.equal(a, b)
+        gdr.beam_select(logits[:1, :, :100], scores[:1], workspace=ws)
+
+
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 def test_select_rows_at_any_address(dt):
     """Rows that start at every offset from 16 bytes, with a stride that moves it from row to row."""
@@ -91,6 +101,28 @@ def test_select_large_values():
     x[0, 1] = torch.arange(3000, device=DEV) * 0.01
     s = torch.tensor([[-1.0, -1.5]], device=DEV)
     check(x, s, gdr.beam_select(x, s))
+
+
+def test_refusals():
+    x, s = logits_of(3, 2, 4, 100, torch.float32)
+    with pytest.raises(gdr.GdrError, match="MODE"):
+        gdr.beam_select(x, s, pad_token=100)
+    with pytest.raises(TypeError):
+        gdr.beam_select(x.half(), s)
+    with pytest.raises(ValueError, match="rows"):
+        gdr.beam_select(x.transpose(0, 1).contiguous().transpose(0, 1), s)
+    with pytest.raises(TypeError):
+        gdr.beam_select(x, s, done=torch.zeros(2, 4, dtype=torch.int32, device=DEV))
+    with pytest.raises(gdr.GdrError, match="UNSUPPORTED"):
+        gdr.beam_select(torch.zeros(1, 33, 10, device=DEV), torch.zeros(1, 33, device=DEV))
+    st, p = torch.zeros(2, 4, 8, device=DEV), torch.zeros(2, 4, dtype=torch.int32, device=DEV)
+    with pytest.raises(gdr.GdrError, match="ALIGN"):
+        gdr.beam_reorder(torch.zeros(2, 4, 3, device=DEV), p)
+    with pytest.raises(ValueError):
+        gdr.beam_reorder(st, p[:1])
+    with pytest.raises(gdr.GdrError, match="ALIAS"):
+        flat = torch.zeros(2 * 4 * 8 + 8, device=DEV)
+        gdr.beam_reorder(flat[:64].view(2, 4, 8), p, out=flat[8:].view(2, 4, 8))
 
 
 def reorder_reference(state, parents, dim):

@@ -131,10 +131,10 @@ def test_backward(shape, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("T", [257, 1100])
-def test_segments(T, dt):
-    """A few heads of a long sequence are walked in segments; the state is updated in place."""
-    x = make(3, [T], 2, 1, 64, 72, dt, g=[-0.003, -0.5])
+@pytest.mark.parametrize("T, H", [(65, 2), (257, 2), (1100, 2), (5000, 1)])
+def test_segments(T, H, dt):
+    """A few heads of a long sequence are walked in segments (64 at most); the state is updated in place."""
+    x = make(3, [T], H, 1, 64, 72, dt, g=[-0.003, -0.5])
     s = x["s0"].clone()
     o, s2 = gdr.head_decay_fwd(x["q"], x["k"], x["v"], x["g"], s0=s, s_final=s)
     assert s2 is s
@@ -165,15 +165,42 @@ def test_packed(lens, dt):
     check_bwd(x, lens, dt, out, 1.0, packed=True)
 
 
-def test_packed_many_sequences():
-    """More sequences than a workgroup has threads."""
+@pytest.mark.parametrize("Dv", [16, 72])
+def test_packed_many_sequences(Dv):
+    """More sequences than a workgroup has threads (256, or 512 for more than 64 columns)."""
     lens = [1 + i % 5 for i in range(600)]
-    x = make(6, lens, 1, 1, 16, 16, "f32", packed=True)
+    x = make(6, lens, 1, 1, 16, Dv, "f32", packed=True)
     o, s = gdr.head_decay_fwd_varlen(x["q"], x["k"], x["v"], x["g"], x["cu"], s0=x["s0"])
     check_fwd(x, lens, "f32", o, s, 1.0, packed=True)
     out = gdr.head_decay_bwd_varlen(x["q"], x["k"], x["v"], x["g"], x["d_o"], x["cu"], s0=x["s0"],
                                     ds_final=x["ds_final"])
     check_bwd(x, lens, "f32", out, 1.0, packed=True)
+
+
+def test_packed_state_in_place():
+    """Segments of a packed batch while s_final is s0."""
+    lens = [700, 3, 450]
+    x = make(21, lens, 2, 2, 64, 64, "bf16", packed=True)
+    s = x["s0"].clone()
+    o, s2 = gdr.head_decay_fwd_varlen(x["q"], x["k"], x["v"], x["g"], x["cu"], s0=s, s_final=s)
+    assert s2 is s
+    check_fwd(x, lens, "bf16", o, s, 1.0, packed=True)
+
+
+def test_long_sequence_in_pieces():
+    """A long sequence at once and in pieces that hand their state on; both are within the tolerance of the exact
+    values, so within twice of each other, and the states' and outputs' A is bounded by the magnitudes' call."""
+    T = 70001
+    x = make(22, [T], 2, 1, 64, 128, "bf16", g=[-0.002, -0.2], s0=False)
+    o, s = gdr.head_decay_fwd(x["q"], x["k"], x["v"], x["g"])
+    A, SA = gdr.head_decay_fwd(x["q"].abs(), x["k"].abs(), x["v"].abs(), x["g"])
+    st, parts = None, []
+    for a, z in ((0, 20000), (20000, 20001), (20001, 61000), (61000, T)):
+        p, st = gdr.head_decay_fwd(*(x[n][:, a:z] for n in "qkv"), x["g"], s0=st)
+        parts.append(p)
+    p = torch.cat(parts, 1)
+    assert torch.all((o.double() - p.double()).abs() <= 2.0 ** -7 * (o.double().abs() + 1.01 * A.double()))
+    assert torch.all((s.double() - st.double()).abs() <= 2.0 ** -13 * 1.01 * SA.double())
 
 
 @pytest.mark.parametrize("cu, spans", [([3, 10, 20], [(3, 10), (10, 20)]), ([-5, 12, 4, 99], [(0, 12), (12, 12), (12, 40)]),
@@ -254,6 +281,76 @@ def test_views_and_broadcasts():
     a = gdr.head_decay_fwd(x["q"], k1, x["v"], x["g"])
     b = gdr.head_decay_fwd(x["q"], k1.contiguous(), x["v"], x["g"])
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_two_calls_at_once():
+    """Calls on two streams without order between them, each with its own workspace."""
+    xs = [make(23 + i, [900], 2, 1, 64, 64, "bf16") for i in range(2)]
+    want = [gdr.head_decay_bwd(x["q"], x["k"], x["v"], x["g"], x["d_o"], s0=x["s0"]) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [[gdr.head_decay_bwd(x["q"], x["k"], x["v"], x["g"], x["d_o"], s0=x["s0"], stream=st)
+            for x, st in zip(xs, streams)] for _ in range(3)]
+    for st in streams:
+        torch.cuda.current_stream().wait_stream(st)
+    for run in got:
+        for a, b in zip(run, want):
+            for n in b:
+                assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("Dk, Dv", [(64, 72), (72, 64), (16, 24), (128, 128), (200, 40), (40, 200), (136, 256)])
+def test_a_workspace_used_again(Dk, Dv, dt):
+    """The contents of a workspace do not matter: filled with NaN, and left by another call."""
+    x = make(25, [700], 2, 1, Dk, Dv, dt)
+    args = [x[n] for n in ("q", "k", "v", "g")]
+    kw = dict(s0=x["s0"], ds_final=x["ds_final"])
+    o, s = gdr.head_decay_fwd(*args, s0=x["s0"])
+    check_fwd(x, [700], dt, o, s, 1.0)
+    want = gdr.head_decay_bwd(*args, x["d_o"], **kw)
+    check_bwd(x, [700], dt, want, 1.0)
+    ws = torch.full((1 << 28,), 255, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        got = gdr.head_decay_fwd(*args, s0=x["s0"], workspace=ws)
+        assert torch.equal(got[0], o) and torch.equal(got[1], s)
+        ws.fill_(255)
+        got = gdr.head_decay_bwd(*args, x["d_o"], workspace=ws, **kw)
+        for n in want:
+            assert torch.equal(got[n], want[n]), n
+    lens = [300, 0, 400]
+    y = make(26, lens, 2, 1, Dk, Dv, dt, packed=True)
+    ws.fill_(255)
+    out = gdr.head_decay_bwd_varlen(y["q"], y["k"], y["v"], y["g"], y["d_o"], y["cu"], s0=y["s0"],
+                                    ds_final=y["ds_final"], workspace=ws)
+    check_bwd(y, lens, dt, out, 1.0, packed=True)
+
+
+def test_refusals():
+    x = make(27, [40], 2, 1, 16, 16, "bf16")
+    with pytest.raises(gdr.GdrError, match="ALIGN"):
+        buf = torch.zeros(40 * 2 * 16 + 1, dtype=torch.bfloat16, device=DEV)
+        gdr.head_decay_fwd(buf[1:].view(1, 40, 2, 16), x["k"], x["v"], x["g"])
+    with pytest.raises(ValueError, match="contiguous"):
+        gdr.head_decay_bwd(x["q"], x["k"], x["v"], x["g"], torch.ones(1, device=DEV).bfloat16().expand(1, 40, 2, 16))
+    with pytest.raises(TypeError):
+        gdr.head_decay_fwd(x["q"], x["k"].float(), x["v"], x["g"])
+    with pytest.raises(TypeError):
+        gdr.head_decay_fwd(x["q"].half(), x["k"].half(), x["v"].half(), x["g"])
+    with pytest.raises(ValueError):
+        gdr.head_decay_fwd(x["q"], x["k"][:, :39], x["v"], x["g"])
+    with pytest.raises(gdr.GdrError, match="ALIAS"):
+        gdr.head_decay_fwd(x["q"], x["k"], x["v"], x["g"], o=x["q"])
+    with pytest.raises(gdr.GdrError, match="WORKSPACE"):
+        y = make(28, [2000], 2, 1, 16, 16, "bf16")
+        gdr.head_decay_fwd(y["q"], y["k"], y["v"], y["g"], workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    st = torch.zeros(1, 2, 16, 16, device=DEV)
+    one = [x[n][:, 0] for n in "qkv"]
+    with pytest.raises(ValueError, match="state_out"):
+        gdr.head_decay_step(*one, x["g"], st, parents=torch.zeros(1, dtype=torch.int32, device=DEV))
+    with pytest.raises(gdr.GdrError, match="SHAPE"):
+        gdr.head_decay_step(*one, x["g"], st.repeat(2, 1, 1, 1))
 
 
 def test_equal_calls_give_equal_bits():
