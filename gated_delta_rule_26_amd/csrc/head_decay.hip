@@ -23,6 +23,8 @@
 // rounded to bf16 before it meets c (relative 2^-9 per pair, of the size of the output's own rounding);
 // the state and the decayed c of the update are split into bf16 hi + lo (2^-17), since the state is fp32
 // for the caller and its errors would add up over the chunks.  With fp32 inputs all products are fp32 MFMAs.
+#include <algorithm>
+
 #include "matrix_common.h"
 #include "ops_internal.h"
 
@@ -857,21 +859,21 @@ hipError_t dispatch(const WalkSet &s, bool bf16, const Shape &sh, hipStream_t st
 
 // ---- sums over the query heads of a group, and of dL/dg's parts
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void group_sum_kernel(const float *__restrict__ src, void *__restrict__ dst,
-                                                             size_t quads, int G, int D) {
+__global__ __launch_bounds__(kThreads) void group_sum_kernel(GroupSum k, GroupSum v, int G) {
+    const GroupSum &s = blockIdx.y == 0 ? k : v;
     const size_t x = (size_t)blockIdx.x * kThreads + threadIdx.x;
-    if (x >= quads) return;
-    const size_t row = x / (D / 4), col = x % (D / 4) * 4;
+    if (x >= s.rows * (s.width / 4)) return;
+    const size_t row = x / (s.width / 4), col = x % (s.width / 4) * 4;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = 0; i < G; ++i) {
-        const float4 y = *reinterpret_cast<const float4 *>(src + (row * G + i) * D + col);
+        const float4 y = *reinterpret_cast<const float4 *>(s.src + (row * G + i) * s.width + col);
         sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
     }
-    const size_t at = row * D + col;
-    store_out<BF16>(dst, at, sum.x);
-    store_out<BF16>(dst, at + 1, sum.y);
-    store_out<BF16>(dst, at + 2, sum.z);
-    store_out<BF16>(dst, at + 3, sum.w);
+    const size_t at = row * s.width + col;
+    store_out<BF16>(s.dst, at, sum.x);
+    store_out<BF16>(s.dst, at + 1, sum.y);
+    store_out<BF16>(s.dst, at + 2, sum.z);
+    store_out<BF16>(s.dst, at + 3, sum.w);
 }
 
 __global__ __launch_bounds__(kThreads) void dg_sum_kernel(const double *__restrict__ part, float *__restrict__ dg,
@@ -907,12 +909,12 @@ hipError_t launch_segment_sums(const WalkSet &s, bool bf16, const Shape &sh, hip
 hipError_t launch_walks(const WalkSet &s, bool bf16, const Shape &sh, bool dg, hipStream_t stream) {
     return dg ? dispatch<kWalkDg>(s, bf16, sh, stream) : dispatch<kWalk>(s, bf16, sh, stream);
 }
-hipError_t launch_group_sum(const float *src, void *dst, bool bf16, size_t rows, int G, int D, hipStream_t stream) {
-    const size_t quads = rows * (D / 4);
+hipError_t launch_group_sums(const GroupSum &k, const GroupSum &v, bool bf16, int G, hipStream_t stream) {
+    const size_t quads = k.rows * (std::max(k.width, v.width) / 4);
     if (quads == 0) return hipSuccess;
-    const dim3 grid((unsigned)((quads + kThreads - 1) / kThreads));
-    if (bf16) hipLaunchKernelGGL(group_sum_kernel<true>, grid, dim3(kThreads), 0, stream, src, dst, quads, G, D);
-    else hipLaunchKernelGGL(group_sum_kernel<false>, grid, dim3(kThreads), 0, stream, src, dst, quads, G, D);
+    const dim3 grid((unsigned)((quads + kThreads - 1) / kThreads), 2);
+    if (bf16) hipLaunchKernelGGL(group_sum_kernel<true>, grid, dim3(kThreads), 0, stream, k, v, G);
+    else hipLaunchKernelGGL(group_sum_kernel<false>, grid, dim3(kThreads), 0, stream, k, v, G);
     return hipGetLastError();
 }
 hipError_t launch_dg_sum(const double *part, float *dg, int units, int H, int slices, int walks, size_t stride,

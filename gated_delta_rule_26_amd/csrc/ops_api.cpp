@@ -351,9 +351,8 @@ int gdr_head_decay_bwd(const gdr_head_decay_desc *d, const int32_t *cu, const vo
         if ((rc = hip_status(gdr::hd::launch_walks(set, bf16, p.sh, false, st))) != GDR_OK) return rc;
     }
     if (shared) {
-        if ((rc = hip_status(gdr::hd::launch_group_sum(at(s.part_k), dk, bf16, tokens * d->Hk, G, d->Dk, st))) != GDR_OK)
-            return rc;
-        return hip_status(gdr::hd::launch_group_sum(at(s.part_v), dv, bf16, tokens * d->Hk, G, d->Dv, st));
+        const gdr::hd::GroupSum sk = {at(s.part_k), dk, tokens * d->Hk, d->Dk}, sv = {at(s.part_v), dv, tokens * d->Hk, d->Dv};
+        return hip_status(gdr::hd::launch_group_sums(sk, sv, bf16, G, st));
     }
     return GDR_OK;
 }

@@ -77,8 +77,14 @@ size_t frag_bytes(const Shape &s, int slices);
 // The segments' sums, and the walks themselves (dg: some of them with parts of dL/dg).
 hipError_t launch_segment_sums(const WalkSet &s, bool bf16, const Shape &sh, hipStream_t stream);
 hipError_t launch_walks(const WalkSet &s, bool bf16, const Shape &sh, bool dg, hipStream_t stream);
-// dst [tokens, Hk, D] = sum over the G query heads of each group of src [tokens, Hk G, D] (fp32).
-hipError_t launch_group_sum(const float *src, void *dst, bool bf16, size_t rows, int G, int D, hipStream_t stream);
+// dst [rows, width] (rows = tokens Hk) = sum over the G query heads of each group of src [rows, G, width], fp32.
+struct GroupSum {
+    const float *src;
+    void *dst;
+    size_t rows;
+    int width;
+};
+hipError_t launch_group_sums(const GroupSum &k, const GroupSum &v, bool bf16, int G, hipStream_t stream);
 // dg[h] = sum over walks, units, slices of part[walk * stride + (unit H + h) slices + slice].
 hipError_t launch_dg_sum(const double *part, float *dg, int units, int H, int slices, int walks, size_t stride,
                          hipStream_t stream);
