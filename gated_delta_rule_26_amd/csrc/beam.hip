@@ -8,8 +8,15 @@
 // lowest beam.  Exponentials are fp32, their sums, the logarithm and the candidates fp64: beams meet at
 // differences far below an fp32 candidate's step.
 //
+// A wavefront's first step bounds what can enter its list from below (the K-th highest of its lanes' maxima, by
+// bisection), so that few of its first 2048 elements are inserted; after it about K / step enter.  Measured: 512
+// rows of 128,003 bf16 logits (131 MB) 49 us + 13 us for the join; without the lists 36 us, without the
+// exponentials 41 us, without both 28 us (the loads).  4 rows of 32,000: 6.5 + 6 us, both kernels latencies.
+//
 // Reordering: a thread keeps its 16 bytes of all K rows of a request in registers between reading and
-// writing, so the rows can be permuted in place, and a row that stays is neither read nor written.
+// writing, so the rows can be permuted in place, and a row that stays is neither read nor written.  Measured: 256
+// states of 1 MiB into a second pool 71 us (about 426 MB: 5.9 TB/s; with ordinary stores and a branch at each load
+// 157 us), 4 MB in place 2.9 us.
 #include <math.h>
 
 #include "ops_internal.h"

@@ -5,24 +5,40 @@
 //   out_i = oscale lambda^i E^T a_i + pscale sum_{j<=i} lambda^{i-j} (a_i . b_j) c_j
 //   E'    = lambda^n E + uscale sum_j lambda^{n-j} b_j c_j^T
 // which is o (a, b, c = q, k, v), dq (d_o, v, k), and in reversed time dv (k, q, d_o) and dk (v, d_o, q).
+// dL/dg = sum_t <dL/dS_t, lambda S_{t-1}> adds, over all pairs of a write and a read, the pair's value times its
+// distance, which is split at the chunks' borders into parts that are each a weighted product the walks have at
+// hand (no difference of large sums): (i - j) inside a chunk, i + 1 from its start, n - 1 - j to its end, and n
+// for pairs across a whole chunk, lambda^n <S, R>, for which dq's walk keeps every chunk's state.
 //
 // Long sequences are cut into segments, so that a few heads fill the card: the first kernel sums each
-// segment's writes from a zero state, U = sum_j lambda^{len-j} b_j c_j^T (exactly the walk without outputs),
-// and the walk of segment s starts from E = lambda^len E + U over the segments before it.
+// segment's writes from a zero state, U = sum_j lambda^{len-j} b_j c_j^T (the walk without outputs), and the
+// walk of segment s starts from E = lambda^len E + U over the segments before it.  dk's states are dv's
+// transposed: their sums are formed once and written twice.
 //
-// One workgroup of four wavefronts walks one segment of one head and a slice of c's columns, 16 NT of them
-// per wavefront, so that the state never leaves the registers: the 16x16 tiles of E that the update's MFMAs
-// accumulate (rows: a's channels, columns: c's) are, lane by lane, the operand of the state's read, when the
-// read's other operand is taken in the permuted order of matrix_common.h.  The pair matrix is shared: its
-// lower 16x16 tiles are spread over the wavefronts, which exchange them through LDS as operand fragments.
-// All outputs are formed transposed (rows: c's channels, columns: tokens), so that the decay of a token is a
-// factor per lane, and the columns of a wavefront's tiles are interleaved so that a lane holds 4 NT
-// consecutive channels of a token: one 16-byte store.
+// One workgroup of eight (up to 64 columns, or rows wider than 128: four) wavefronts walks one segment of one
+// head and a slice of c's columns, 16 of them per wavefront, so that the state never leaves the registers: the
+// 16x16 tiles of E that the update's MFMAs accumulate (rows: a's channels, columns: c's) are, lane by lane, the
+// operand of the state's read, when the read's other operand is taken in the permuted order of matrix_common.h.
+// The pair matrix is shared: its lower 16x16 tiles are spread over the wavefronts, which exchange them through
+// LDS as operand fragments.  All outputs are formed transposed (rows: c's channels, columns: tokens), so that the
+// decay of a token is a factor per lane and a lane holds consecutive channels of a token.  The rows of the next
+// chunk are loaded into registers while this one is computed.
 //
-// Roundings below fp32 with bf16 inputs (products of bf16 values are exact in fp32): the pair matrix is
-// rounded to bf16 before it meets c (relative 2^-9 per pair, of the size of the output's own rounding);
-// the state and the decayed c of the update are split into bf16 hi + lo (2^-17), since the state is fp32
-// for the caller and its errors would add up over the chunks.  With fp32 inputs all products are fp32 MFMAs.
+// Roundings below fp32 with bf16 inputs (products of bf16 values are exact in fp32): the pair matrix is rounded
+// to bf16 before it meets c (2^-8 of each pair at most, of the size of the output's own rounding); the state's
+// read takes it as bf16 hi + lo (2^-16): dropping lo would add an error of the output rounding's size, for 5 %
+// of the time; the decayed c of the update is hi + mid + lo, 24 bits, since the state is fp32 for the caller and its
+// errors would add up over the chunks.  With fp32 inputs all products are fp32 MFMAs.
+//
+// Measured on one MI355X (bf16, 16 heads of 128 x 128; a copy reaches 5.5 TB/s):
+//   4 x 4096 tokens forward: sums 39 us + walks 85 us for 273 MB (floor 50 us).  Without its products the walk
+//   takes 63 us (its loads, stores and start), without its loads 77 us: it is bound by both, the products of a
+//   chunk (94 MFMAs and 340 vector instructions a wavefront, 420 KB of LDS reads in all) a little more.
+//   2 x 8192 tokens backward, fixed decays: sums 85 us + three walks 185 us (floor 86 us).
+// Not better: 32 columns a wavefront on four wavefronts (the same time), slices of 64 columns (the pair matrix
+// twice: 108 against 91 us), more segments than the card holds at once (512 -> 768 workgroups: 118 -> 130 us), heads
+// of a segment on one XCD (the same), two chunks of loads ahead in the sums (the same).  Anything that makes the
+// register allocator spill inside the loop costs 15 %: a reload waits for all loads on the way.
 #include <algorithm>
 
 #include "matrix_common.h"

@@ -6,6 +6,9 @@
 // takes one (sequence, head) or a slice of its columns, so that a few sequences still fill the card.
 // A thread holds four columns of every RPP-th row (one 16-byte access each, rows contiguous).
 //
+// Measured: 256 sequences x 16 heads of 128 x 128 (541 MB) 99-103 us, 5.3-5.5 TB/s, what a copy reaches;
+// 8 beams x 8 heads of 64 x 64 (2.1 MB) 4.8 us, two latencies of memory and the launch.
+//
 // A search's beams continue from their parents' states: reading row parents[n] here instead of moving the
 // states first saves a pass over them.
 #include "ops_internal.h"

@@ -85,7 +85,10 @@ int check_view(const void *p, const int64_t *stride, int B, int T, int heads, in
 // How a call is cut up.  A workgroup walks a segment of a head and a column slice.  A segment costs a second
 // reading of b and c and its sum, and all of them pay for a round of workgroups that is not full: so there are as
 // many segments as fill the card once (what is resident at a time), of 64 tokens at least, and kMaxSegments per
-// sequence at most (each starts from a chain of sums).
+// sequence at most (each starts from a chain of sums).  Measured: 1.5 times as many workgroups as the card holds
+// 118 -> 130 us (prefill of 4 x 4096 tokens, 16 heads of 128 x 128), 5 segments instead of 6 for the backward pass
+// of 2 x 8192 tokens (480 instead of 576 workgroups) 325 -> 273 us; segments of 64 instead of 256 tokens at least
+// 171 -> 78 us (backward pass of 2 x 777 tokens, 4 heads).
 struct Plan {
     Shape sh;
     int slices;
