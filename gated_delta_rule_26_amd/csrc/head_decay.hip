@@ -34,7 +34,7 @@
 //   4 x 4096 tokens forward: sums 39 us + walks 85 us for 273 MB (floor 50 us).  Without its products the walk
 //   takes 63 us (its loads, stores and start), without its loads 77 us: it is bound by both, the products of a
 //   chunk (94 MFMAs and 340 vector instructions a wavefront, 420 KB of LDS reads in all) a little more.
-//   2 x 8192 tokens backward, fixed decays: sums 85 us + three walks 185 us (floor 86 us).
+//   2 x 8192 tokens backward, fixed decays: sums 83 us + three walks 187 us (floor 86 us).
 // Not better: 32 columns a wavefront on four wavefronts (the same time), slices of 64 columns (the pair matrix
 // twice: 108 against 91 us), more segments than the card holds at once (512 -> 768 workgroups: 118 -> 130 us), heads
 // of a segment on one XCD (the same), two chunks of loads ahead in the sums (the same).  Anything that makes the
@@ -138,13 +138,14 @@ __device__ Place find_place(const Batch &b, int u, PlaceSmem &sm) {
             if (u > 0 && u < units) break;
         }
         __syncthreads();
-        p.last = top;
-        p.n = sm.found[0];
-        p.tok0 = sm.found[1];
-        p.seq_len = sm.found[2];
-        p.s = sm.found[3];
-        p.ns = sm.found[4];
-        p.chunk0 = sm.found[5];
+        // the same in all lanes: kept in scalar registers
+        p.last = __builtin_amdgcn_readfirstlane(top);
+        p.n = __builtin_amdgcn_readfirstlane(sm.found[0]);
+        p.tok0 = __builtin_amdgcn_readfirstlane(sm.found[1]);
+        p.seq_len = __builtin_amdgcn_readfirstlane(sm.found[2]);
+        p.s = __builtin_amdgcn_readfirstlane(sm.found[3]);
+        p.ns = __builtin_amdgcn_readfirstlane(sm.found[4]);
+        p.chunk0 = __builtin_amdgcn_readfirstlane(sm.found[5]);
         if (p.n < 0) return p;
     }
     p.t0 = p.s * b.seg;
@@ -179,7 +180,9 @@ __device__ __forceinline__ f32x4 mul_add(f32x4 a, f32x4 b, f32x4 c) {
 
 // ---- a tile of ROWS tokens x W channels: global -> registers -> LDS, 16 bytes a lane.  Orders of the channels
 // in LDS, so that both the 16-byte accesses of rows and the transposing reads of 4x16 blocks take every bank once:
-//   kRows     read by rows only.  bf16: each 32-block in the order of kperm, a fragment being one 16-byte read
+//   kRows     read by rows only.  bf16: the fragments of lane group lg, 16 bytes a row and 32-block, in a plane of
+//             their own, rows an odd number of 16-byte pieces long: any 16 rows' reads take all banks, whichever
+//             lane groups they are read by
 //   kBoth     read by rows and transposed: as they come
 //   kColumns  read transposed only, in column tiles of NT interleaved ones: the quads of each 16 NT channels
 //             sorted by tile
@@ -196,6 +199,10 @@ struct Tile {
     static constexpr int passes = ROWS / rpp;
     static constexpr int ld = W + (BF16 ? (ORD == kRows ? 8 : 16) : 4);
     static_assert(64 * WV % pieces == 0 && ROWS % rpp == 0, "tile must divide among the threads");
+    // kRows of bf16: elements of a row in a plane, and of a plane (planes 2 and 3 half the banks further)
+    static constexpr int prow = 8 * (W / 32 + 1), plane = ROWS * prow;
+    static constexpr int size = BF16 && ORD == kRows ? 4 * plane + 64 : ROWS * ld;  // elements in LDS
+    static_assert(ORD != kRows || !BF16 || (prow % 16 == 8 && plane % 128 == 0), "planes start at the same bank");
     uint4 r[passes];
 
     // This thread's first byte of a chunk of `stride` bytes a row, out of any chunk's range where the channel
@@ -224,8 +231,13 @@ struct Tile {
         for (int i = 0; i < passes; ++i) {
             typename T::lds *row = s + (r0 + i * rpp) * ld;
             if constexpr (BF16 && ORD == kRows) {
-                *reinterpret_cast<uint2 *>(row + mx::kperm_col(pc, 0)) = make_uint2(r[i].x, r[i].y);
-                *reinterpret_cast<uint2 *>(row + mx::kperm_col(pc, 1)) = make_uint2(r[i].z, r[i].w);
+                // channels 8 pc .. + 7 of the row: quads 2 q and 2 q + 1 of a 32-block (q = pc % 4), of which quad
+                // j is the first (j < 4) or second half of lane group j % 4's fragment
+                const int q = pc & 3;
+                typename T::lds *at = s + (r0 + i * rpp) * prow + 8 * (pc >> 2) + 4 * (q >> 1);
+                const int to = (2 * q) & 3;
+                *reinterpret_cast<uint2 *>(at + to * plane + 32 * to) = make_uint2(r[i].x, r[i].y);
+                *reinterpret_cast<uint2 *>(at + (to + 1) * plane + 32 * to) = make_uint2(r[i].z, r[i].w);
             } else if constexpr (ORD == kColumns && NT == 2) {
                 if constexpr (BF16) {
                     typename T::lds *at = row + 32 * (pc >> 2) + 4 * (pc & 3);
@@ -244,14 +256,14 @@ struct Tile {
 __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 c) {
     return bf16x8{a[0], a[1], a[2], a[3], c[0], c[1], c[2], c[3]};
 }
-// Fragment of row `row`, channel block kb.
-template <bool BF16, Order ORD>
-__device__ __forceinline__ typename El<BF16>::frag row_frag(const typename El<BF16>::lds *s, int ld, int row, int kb,
-                                                            int lg) {
+// Fragment of row `row`, channel block kb, of a tile of the type TILE.
+template <bool BF16, Order ORD, typename TILE>
+__device__ __forceinline__ typename El<BF16>::frag row_frag(const typename El<BF16>::lds *s, int row, int kb, int lg) {
+    constexpr int ld = TILE::ld;
     if constexpr (!BF16) {
         return *reinterpret_cast<const f32x4 *>(s + row * ld + 16 * kb + 4 * lg);
     } else if constexpr (ORD == kRows) {
-        return *reinterpret_cast<const bf16x8 *>(s + row * ld + 32 * kb + 8 * lg);
+        return *reinterpret_cast<const bf16x8 *>(s + lg * TILE::plane + 64 * (lg >> 1) + row * TILE::prow + 8 * kb);
     } else {
         const __bf16 *at = s + row * ld + 32 * kb + 4 * lg;
         return join(*reinterpret_cast<const bf16x4 *>(at), *reinterpret_cast<const bf16x4 *>(at + 16));
@@ -323,7 +335,7 @@ template <bool BF16, int PAD, int NT, int CH, int WV, int MODE>
 struct Smem {
     using L = typename El<BF16>::lds;
     static constexpr int nfrag = BF16 ? (CH == 64 ? 6 : 2) : (CH / 16) * (CH / 16);
-    __align__(16) L a[MODE == kSums ? 1 : CH * Tile<BF16, PAD, CH, kRows, 1, WV>::ld];
+    __align__(16) L a[MODE == kSums ? 1 : Tile<BF16, PAD, CH, kRows, 1, WV>::size];
     __align__(16) L b[CH * Tile<BF16, PAD, CH, kBoth, 1, WV>::ld];
     __align__(16) L c[CH * Tile<BF16, 16 * NT * WV, CH, kColumns, NT, WV>::ld];
     __align__(16) char p[MODE == kSums ? 16 : nfrag * 1024];
@@ -348,7 +360,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     using TileA = Tile<BF16, PAD, CH, kRows, 1, WV>;
     using TileB = Tile<BF16, PAD, CH, kBoth, 1, WV>;
     using TileC = Tile<BF16, COLS, CH, kColumns, NT, WV>;
-    constexpr int LDA = TileA::ld, LDB = TileB::ld, LDC = TileC::ld;
+    constexpr int LDB = TileB::ld, LDC = TileC::ld;
     __shared__ Smem<BF16, PAD, NT, CH, WV, MODE> sm;
 
     const Walk &w = set.w[blockIdx.y];
@@ -365,8 +377,8 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
         const int es = w.out_f32 ? 4 : T::bytes, per = 16 / es;
         const int cols = min(COLS, w.Dc - slice * COLS);
         const int outside = pl.first + (b.T - pl.last);
-        for (int x = tid; x < outside * (cols / per); x += 64 * WV) {
-            const int i = x / (cols / per), row = i < pl.first ? i : pl.last + (i - pl.first);
+        for (int64_t x = tid; x < (int64_t)outside * (cols / per); x += 64 * WV) {
+            const int i = (int)(x / (cols / per)), row = i < pl.first ? i : pl.last + (i - pl.first);
             char *dst = w.out + (((int64_t)row * b.H + h) * w.Dc + slice * COLS + (x % (cols / per)) * per) * es;
             *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
         }
@@ -550,8 +562,8 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
             for (int kb = 0; kb < KD; ++kb)
 #pragma unroll
                 for (int q = 0; q < PT; ++q)
-                    acc[q] = mul_add(row_frag<BF16, kBoth>(sm.b, LDB, 16 * tile_j[q] + lr, kb, lg),
-                                     row_frag<BF16, kRows>(sm.a, LDA, 16 * tile_i[q] + lr, kb, lg), acc[q]);
+                    acc[q] = mul_add(row_frag<BF16, kBoth, TileB>(sm.b, 16 * tile_j[q] + lr, kb, lg),
+                                     row_frag<BF16, kRows, TileA>(sm.a, 16 * tile_i[q] + lr, kb, lg), acc[q]);
 #pragma unroll
             for (int q = 0; q < PT; ++q) {
                 const int I = tile_i[q], J = tile_j[q], apart = I - J;
@@ -600,7 +612,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
                 }
 #pragma unroll
                 for (int I = 0; I < CI; ++I) {
-                    const frag af = row_frag<BF16, kRows>(sm.a, LDA, 16 * I + lr, kb, lg);
+                    const frag af = row_frag<BF16, kRows, TileA>(sm.a, 16 * I + lr, kb, lg);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         O[I][nt] = mul_add(hi[nt], af, O[I][nt]);
