@@ -63,6 +63,8 @@ def _device(q):
 def _check_any(name, t, device, dtype, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if (t.device, t.dtype, t.shape) == (device, dtype, shape):
+        return
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if dtype is not None and t.dtype != dtype:
@@ -74,7 +76,7 @@ def _check_any(name, t, device, dtype, shape):
 def _check_view(name, t, device, dtype, shape):
     """A tensor that may be strided, but for its last dimension."""
     _check_any(name, t, device, dtype, shape)
-    if t.stride(-1) != 1 and shape[-1] > 1 and t.numel() > 0:
+    if t.stride(-1) != 1 and shape[-1] > 1 and t.numel() > 0:  # (strides of nothing do not matter)
         raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
@@ -84,6 +86,7 @@ def _check_dev(name, t, device, dtype=None, shape=None):
         raise ValueError(f"{name} must be contiguous")
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 # the handle of torch's current stream, without the Stream object around it where torch offers that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -102,7 +105,7 @@ def _strides(t, dims):
 def _call(dev, name, *args):
     """The library call, on the tensors' device."""
     fn = getattr(load_library(), name)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -151,16 +154,16 @@ def head_decay_bwd_workspace_size(desc: HeadDecayDesc, packed: bool = False, nee
 
 @functools.lru_cache(maxsize=1024)
 def _described(kind, need_dg, B, T, H, Hk, Dk, Dv, dtype, scale, *strides):
-    """(descriptor, workspace bytes) of a call: both follow from sizes and strides alone, and a program's calls
-    repeat them.  kind: "fwd", "bwd" (a second letter p: packed) or "step"."""
+    """(reference to the descriptor, workspace bytes) of a call: both follow from sizes and strides alone, and a
+    program's calls repeat them.  kind: "fwd", "bwd" (a second letter p: packed) or "step"."""
     desc = make_head_decay_desc(B, T, H, Hk, Dk, Dv, dtype=dtype, scale=scale, q_stride=strides[0],
                                 k_stride=strides[1], v_stride=strides[2],
                                 do_stride=strides[3] if len(strides) > 3 else (0, 0, 0))
     if kind == "step":
-        return desc, 0
+        return ctypes.byref(desc), 0
     if kind.startswith("fwd"):
-        return desc, head_decay_fwd_workspace_size(desc, kind == "fwdp")
-    return desc, head_decay_bwd_workspace_size(desc, kind == "bwdp", need_dg)
+        return ctypes.byref(desc), head_decay_fwd_workspace_size(desc, kind == "fwdp")
+    return ctypes.byref(desc), head_decay_bwd_workspace_size(desc, kind == "bwdp", need_dg)
 
 
 def _tokens(q, k, v, g, cu_seqlens):
@@ -214,7 +217,7 @@ def _fwd(q, k, v, g, cu_seqlens, scale, s0, output_final_state, s_final, o, work
                             _strides(q, dims), _strides(k, dims), _strides(v, dims))
     workspace = _workspace(workspace, need, dev, fresh)
     st = _on(stream, dev, fresh)
-    _call(dev, "gdr_head_decay_fwd", ctypes.byref(desc), _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+    _call(dev, "gdr_head_decay_fwd", desc, _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
           _ptr(s0), _ptr(o), _ptr(s_final), _ptr(workspace), 0 if workspace is None else workspace.numel(),
           st)
     return o, s_final
@@ -267,7 +270,7 @@ def _bwd(q, k, v, g, d_o, cu_seqlens, scale, s0, ds_final, need_dg, need_ds0, wo
                             _strides(q, dims), _strides(k, dims), _strides(v, dims), _strides(d_o, dims))
     workspace = _workspace(workspace, need, dev, fresh)
     st = _on(stream, dev, fresh)
-    _call(dev, "gdr_head_decay_bwd", ctypes.byref(desc), _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+    _call(dev, "gdr_head_decay_bwd", desc, _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
           _ptr(s0), _ptr(d_o), _ptr(ds_final), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]),
           _ptr(out["ds0"]), _ptr(workspace), 0 if workspace is None else workspace.numel(),
           st)
@@ -340,7 +343,7 @@ def head_decay_step(q, k, v, g, state, *, scale: float = 1.0, slots=None, parent
     desc, _ = _described("step", False, N, 1, H, Hk, Dk, Dv, q.dtype, float(scale), _strides(q, 1), _strides(k, 1),
                          _strides(v, 1))
     st = _on(stream, dev, fresh)
-    _call(dev, "gdr_head_decay_step", ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state),
+    _call(dev, "gdr_head_decay_step", desc, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state),
           state.shape[0], _ptr(slots), _ptr(parents), _ptr(state_out), _ptr(o), st)
     return o
 

@@ -193,6 +193,40 @@ def test_search_over_decode_steps():
             assert torch.equal(y, z)
 
 
+def test_search_over_delta_rule_steps():
+    """The same around the library's other decode step: recurrent_step keeps its states in place, the selection's
+    parents move them (all layers at once), and each beam goes on as a decode from a copy of its parent's state."""
+    L, B, K, H, D, V = 2, 2, 3, 2, 64, 61
+    N = B * K
+    gen = torch.Generator(DEV).manual_seed(9)
+    table = torch.randn(V, 3, H, D, generator=gen, device=DEV) * 0.3
+    head = torch.randn(H * D, V, generator=gen, device=DEV) * 0.1
+    g = torch.full((N, H), -0.05, device=DEV)
+    beta = torch.full((N, H), 0.5, device=DEV)
+    states = torch.randn(L, B, 1, H, D, D, generator=gen, device=DEV).expand(L, B, K, H, D, D).contiguous()
+    copies = states.clone()
+    scores = torch.tensor([[0.0] + [-float("inf")] * (K - 1)] * B, device=DEV)
+    tokens = torch.zeros(B, K, dtype=torch.int32, device=DEV)
+
+    def step(state):
+        x = table[tokens.long().flatten()]
+        for layer in range(L):
+            q, k, v = (y.contiguous() for y in x.unbind(1))
+            o = gdr.recurrent_step(q, k, v, g, beta, state[layer].view(N, H, D, D))
+            x = x + o[:, None]
+        return (o.flatten(1).double() @ head.double()).float().view(B, K, V)
+
+    for _ in range(4):
+        logits = step(states)
+        assert torch.equal(step(copies), logits)
+        was = scores
+        scores, tokens, parents, done = gdr.beam_select(logits, was)
+        check(logits, was, (scores, tokens, parents, done))
+        gdr.beam_reorder(states, parents, dim=1)
+        copies = reorder_reference(copies, parents, 1).contiguous()
+        assert torch.equal(states, copies)
+
+
 def test_graph_and_stream():
     logits, scores = logits_of(6, 2, 4, 3001, torch.bfloat16)
     state = torch.randn(2, 4, 8, 16, device=DEV)
