@@ -104,8 +104,9 @@ int make_plan(const gdr_head_decay_desc *d, bool packed, int wide, int cols, int
     const int64_t share = (int64_t)kFill * p->sh.resident / std::max<int64_t>((int64_t)d->H * p->slices * walks, 1);
     int64_t seg, per = 1;
     if (packed) {
-        // a sequence's last segment is half full on average
-        seg = T / std::max<int64_t>(share - d->B / 2, 1);
+        // a sequence's last segment is half full on average; with many sequences the long ones among them are
+        // still cut
+        seg = T / std::max<int64_t>(std::max<int64_t>(share - d->B / 2, share / 2), 1);
         seg = std::max(seg, (T + gdr::hd::kMaxSegments - 1) / gdr::hd::kMaxSegments);
     } else {
         per = std::min<int64_t>(std::max<int64_t>(share / std::max(d->B, 1), 1), gdr::hd::kMaxSegments);

@@ -177,6 +177,16 @@ def test_packed_many_sequences(Dv):
     check_bwd(x, lens, "f32", out, 1.0, packed=True)
 
 
+def test_packed_one_long_among_many():
+    lens = [5] * 40 + [1500] + [3] * 40
+    x = make(29, lens, 8, 4, 16, 24, "bf16", packed=True)
+    o, s = gdr.head_decay_fwd_varlen(x["q"], x["k"], x["v"], x["g"], x["cu"], s0=x["s0"])
+    check_fwd(x, lens, "bf16", o, s, 1.0, packed=True)
+    out = gdr.head_decay_bwd_varlen(x["q"], x["k"], x["v"], x["g"], x["d_o"], x["cu"], s0=x["s0"],
+                                    ds_final=x["ds_final"])
+    check_bwd(x, lens, "bf16", out, 1.0, packed=True)
+
+
 def test_packed_state_in_place():
     """Segments of a packed batch while s_final is s0."""
     lens = [700, 3, 450]
