@@ -546,6 +546,42 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
         if ((x < 2 || n < CH || less) && tid < CH) sm.write[tid] = tid < n ? sm.rpow[CH - n + less + tid] * w.uscale : 0.f;
         if (x + 1 < chunks) fetch(x + 1);
         mx::barrier_lds();
+        // the state that dq's walk kept of this chunk, on the way while the pairs and the state's read are formed
+        const size_t kept_at = ((size_t)(pl.chunk0 + ci) * b.H + h) * set.slices + slice;
+        f32x4 kept[DG ? TT : 1][NT];
+        if constexpr (DG) {
+            if (w.chunk_e && w.reverse) {
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) kept[t][nt] = *fragments(w.chunk_e, kept_at, t, nt);
+            }
+        }
+        // and the lane's part of the rows of x: four channels of each token and column tile
+        f32x4 xr[DG ? CI : 1][NT];
+        if constexpr (DG) {
+            if (w.x.p) {
+                const char *px = view(w.x);
+#pragma unroll
+                for (int I = 0; I < CI; ++I)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int i = 16 * I + lr, col = col0 + 4 * NT * lg + 4 * nt;
+                        xr[I][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        if (i < n && col < w.Dc) {
+                            const int64_t row = ci * CH + (w.reverse ? n - 1 - i : i);
+                            const char *at = px + row * w.x.tok + (int64_t)col * T::bytes;
+                            if constexpr (BF16) {
+                                const uint2 y = *reinterpret_cast<const uint2 *>(at);
+                                xr[I][nt] = f32x4{__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u),
+                                                  __uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u)};
+                            } else {
+                                xr[I][nt] = *reinterpret_cast<const f32x4 *>(at);
+                            }
+                        }
+                    }
+            }
+        }
 
         if constexpr (OUT) {
             // pair tiles (I, J), J <= I, transposed (rows: tokens j, columns: tokens i)
@@ -632,19 +668,16 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
 
         if constexpr (DG) {
             if (w.chunk_e) {
-                const size_t index = ((size_t)(pl.chunk0 + ci) * b.H + h) * set.slices + slice;
                 float sum = 0.f;
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        f32x4 *at = fragments(w.chunk_e, index, t, nt);
                         if (!w.reverse) {
-                            *at = E[t][nt];
+                            *fragments(w.chunk_e, kept_at, t, nt) = E[t][nt];
                         } else {
-                            const f32x4 e = *at;
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) sum += e[r] * E[t][nt][r];
+                            for (int r = 0; r < 4; ++r) sum += kept[t][nt][r] * E[t][nt][r];
                         }
                     }
                 // pairs across the whole chunk: n lambda^n <S, R>, and the stored E is lambda S
@@ -671,22 +704,16 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
             // direction that the pairs decay)
             if (w.x.p) {
                 float sum = 0.f;
-                const char *px = view(w.x);
 #pragma unroll
                 for (int I = 0; I < CI; ++I) {
                     const int i = 16 * I + lr;
+                    const float f = static_cast<float>(w.reverse ? i : i + 1);
                     if (i < n) {
-                        const int64_t row = ci * CH + (w.reverse ? n - 1 - i : i);
-                        const float f = static_cast<float>(w.reverse ? i : i + 1);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const int col = col0 + 4 * NT * lg + 4 * nt;
-                            if (col < w.Dc) {
-                                const char *at = px + row * w.x.tok + (int64_t)col * T::bytes;
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int r = 0; r < 4; ++r) sum += f * load_in<BF16>(at, r) * O[I][nt][r];
-                            }
-                        }
+                            for (int r = 0; r < 4; ++r)
+                                if (col0 + 4 * NT * lg + 4 * nt < w.Dc) sum += f * xr[I][nt][r] * O[I][nt][r];
                     }
                 }
                 dg += static_cast<double>(sum);
@@ -793,14 +820,13 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
                         __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, ro, (int)off, 0, 0);
                 }
                 if constexpr (DG) {
-                    const int i = 16 * I + lr, col = col0 + 4 * NT * lg;
-                    if (weighted && i < n && col < w.Dc) {
-                        const char *px = view(w.x) + (int64_t)(ci * CH + i) * w.x.tok + (int64_t)col * T::bytes;
+                    if (weighted && 16 * I + lr < n) {
                         float sum = 0.f;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) sum += load_in<BF16>(px, 4 * nt + r) * Y[I][nt][r];
+                            for (int r = 0; r < 4; ++r)
+                                if (col0 + 4 * NT * lg + 4 * nt < w.Dc) sum += xr[I][nt][r] * Y[I][nt][r];
                         dg += static_cast<double>(sum);
                     }
                 }
