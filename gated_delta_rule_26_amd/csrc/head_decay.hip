@@ -184,13 +184,12 @@ __device__ __forceinline__ f32x4 mul_add(f32x4 a, f32x4 b, f32x4 c) {
 //             their own, rows an odd number of 16-byte pieces long: any 16 rows' reads take all banks, whichever
 //             lane groups they are read by
 //   kBoth     read by rows and transposed: as they come
-//   kColumns  read transposed only, in column tiles of NT interleaved ones: the quads of each 16 NT channels
-//             sorted by tile
+//   kColumns  read transposed only: as they come
 // (bf16 rows of kBoth and kColumns are 8 words longer than a multiple of the banks: the 8 rows x 32 bytes of a
 // transposing read's half lie side by side.)
 enum Order { kRows, kBoth, kColumns };
 
-template <bool BF16, int W, int ROWS, Order ORD, int NT, int WV>
+template <bool BF16, int W, int ROWS, Order ORD, int WV>
 struct Tile {
     using T = El<BF16>;
     static constexpr int per = 16 / T::bytes;       // elements of a piece
@@ -238,14 +237,6 @@ struct Tile {
                 const int to = (2 * q) & 3;
                 *reinterpret_cast<uint2 *>(at + to * plane + 32 * to) = make_uint2(r[i].x, r[i].y);
                 *reinterpret_cast<uint2 *>(at + (to + 1) * plane + 32 * to) = make_uint2(r[i].z, r[i].w);
-            } else if constexpr (ORD == kColumns && NT == 2) {
-                if constexpr (BF16) {
-                    typename T::lds *at = row + 32 * (pc >> 2) + 4 * (pc & 3);
-                    *reinterpret_cast<uint2 *>(at) = make_uint2(r[i].x, r[i].y);
-                    *reinterpret_cast<uint2 *>(at + 16) = make_uint2(r[i].z, r[i].w);
-                } else {
-                    *reinterpret_cast<uint4 *>(row + 32 * (pc >> 3) + 16 * (pc & 1) + 4 * ((pc & 7) >> 1)) = r[i];
-                }
             } else {
                 *reinterpret_cast<uint4 *>(row + pc * per) = r[i];
             }
@@ -331,13 +322,13 @@ __device__ __forceinline__ int pair_frag(int I, int kb) {
 
 enum { kSums = 0, kWalk = 1, kWalkDg = 2 };
 
-template <bool BF16, int PAD, int NT, int CH, int WV, int MODE>
+template <bool BF16, int PAD, int CH, int WV, int MODE>
 struct Smem {
     using L = typename El<BF16>::lds;
     static constexpr int nfrag = BF16 ? (CH == 64 ? 6 : 2) : (CH / 16) * (CH / 16);
-    __align__(16) L a[MODE == kSums ? 1 : Tile<BF16, PAD, CH, kRows, 1, WV>::size];
-    __align__(16) L b[CH * Tile<BF16, PAD, CH, kBoth, 1, WV>::ld];
-    __align__(16) L c[CH * Tile<BF16, 16 * NT * WV, CH, kColumns, NT, WV>::ld];
+    __align__(16) L a[MODE == kSums ? 1 : Tile<BF16, PAD, CH, kRows, WV>::size];
+    __align__(16) L b[CH * Tile<BF16, PAD, CH, kBoth, WV>::ld];
+    __align__(16) L c[CH * Tile<BF16, 16 * WV, CH, kColumns, WV>::ld];
     __align__(16) char p[MODE == kSums ? 16 : nfrag * 1024];
     __align__(16) char ph[MODE == kWalkDg ? nfrag * 1024 : 16];  // (i - j) times the pair matrix, hi
     __align__(16) char pl[MODE == kWalkDg ? nfrag * 1024 : 16];  // and lo
@@ -347,7 +338,7 @@ struct Smem {
     PlaceSmem place;
 };
 
-template <bool BF16, int PAD, int NT, int CH, int WV, int MODE>
+template <bool BF16, int PAD, int CH, int WV, int MODE>
 __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void walk_kernel(WalkSet set) {
     using T = El<BF16>;
     using frag = typename T::frag;
@@ -355,13 +346,13 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     constexpr int KT = CH / T::depth;    // token blocks of a chunk
     constexpr int CI = CH / 16;          // token tiles of a chunk
     constexpr int TT = PAD / 16;         // row tiles of the state
-    constexpr int COLS = 16 * NT * WV;
+    constexpr int COLS = 16 * WV;
     constexpr bool OUT = MODE != kSums, DG = MODE == kWalkDg;
-    using TileA = Tile<BF16, PAD, CH, kRows, 1, WV>;
-    using TileB = Tile<BF16, PAD, CH, kBoth, 1, WV>;
-    using TileC = Tile<BF16, COLS, CH, kColumns, NT, WV>;
+    using TileA = Tile<BF16, PAD, CH, kRows, WV>;
+    using TileB = Tile<BF16, PAD, CH, kBoth, WV>;
+    using TileC = Tile<BF16, COLS, CH, kColumns, WV>;
     constexpr int LDB = TileB::ld, LDC = TileC::ld;
-    __shared__ Smem<BF16, PAD, NT, CH, WV, MODE> sm;
+    __shared__ Smem<BF16, PAD, CH, WV, MODE> sm;
 
     const Walk &w = set.w[blockIdx.y];
     const Batch &b = set.b;
@@ -372,7 +363,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     const int u = group / b.H, h = group - u * b.H;
     const Place pl = find_place<CH, DG, WV>(b, u, sm.place);
     const size_t part = ((size_t)u * b.H + h) * set.slices + slice;  // of u, chunk_e, dg_part
-    const int col0 = slice * COLS + wv * 16 * NT;                    // the wavefront's first column
+    const int col0 = slice * COLS + wv * 16;                         // the wavefront's first column
     if (OUT && b.cu && w.zero_outside && u == 0) {
         const int es = w.out_f32 ? 4 : T::bytes, per = 16 / es;
         const int cols = min(COLS, w.Dc - slice * COLS);
@@ -396,7 +387,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     auto lam = [&](int x) { return sm.rpow[CH - x]; };  // lambda^x, 0 <= x <= CH
     if constexpr (OUT && BF16) {
         // the upper tiles inside the fragments' 32-blocks stay zero
-        for (int x = tid; x < Smem<BF16, PAD, NT, CH, WV, MODE>::nfrag * 64; x += 64 * WV) {
+        for (int x = tid; x < Smem<BF16, PAD, CH, WV, MODE>::nfrag * 64; x += 64 * WV) {
             const int I = CI == 2 ? x / 64 : mx::frag_M(x / 64), kb = CI == 2 ? 0 : mx::frag_kb(x / 64);
             if (2 * kb + 1 > I) {
                 *reinterpret_cast<uint4 *>(sm.p + x * 16) = make_uint4(0, 0, 0, 0);
@@ -438,63 +429,55 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     if (early && chunks > 0) fetch(0);
 
     // ---- the entering state
-    const int mcol = 4 * NT * (lr >> 2) + (lr & 3);  // lane's column in tile 0 of the wavefront's columns
-    const size_t e_base = ((size_t)pl.n * b.H + h) * w.Da * w.Dc;
-    f32x4 E[TT][NT];
+        const size_t e_base = ((size_t)pl.n * b.H + h) * w.Da * w.Dc;
+    f32x4 E[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) E[t][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto fragments = [&](float *base, size_t index, int t, int nt) {
-        return reinterpret_cast<f32x4 *>(base + index * (size_t)(PAD * COLS)) + ((wv * TT + t) * NT + nt) * 64 + lane;
+        E[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto fragments = [&](float *base, size_t index, int t) {
+        return reinterpret_cast<f32x4 *>(base + index * (size_t)(PAD * COLS)) + (wv * TT + t) * 64 + lane;
     };
     if constexpr (OUT) {
         if (w.e0) {
             const float f = w.e0_decay ? lam(1) : 1.f;
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
+            for (int t = 0; t < TT; ++t) {
+                const int row = 16 * t + 4 * lg, col = col0 + lr;
+                if (row < w.Da && col < w.Dc) {
+                    if (w.e0_t) {
+                        E[t] = *reinterpret_cast<const f32x4 *>(w.e0 + e_base + (size_t)col * w.Da + row);
+                    } else {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int row = 16 * t + 4 * lg, col = col0 + mcol + 4 * nt;
-                    if (row < w.Da && col < w.Dc) {
-                        if (w.e0_t) {
-                            E[t][nt] = *reinterpret_cast<const f32x4 *>(w.e0 + e_base + (size_t)col * w.Da + row);
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) E[t][nt][r] = w.e0[e_base + (size_t)(row + r) * w.Dc + col];
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) E[t][nt][r] *= f;
+                        for (int r = 0; r < 4; ++r) E[t][r] = w.e0[e_base + (size_t)(row + r) * w.Dc + col];
                     }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) E[t][r] *= f;
                 }
+            }
         }
     }
     if constexpr (OUT) {
         // the segments before this one, two of them in flight
         const int before = w.reverse ? pl.ns - 1 - pl.s : pl.s;
         auto number = [&](int x) { return w.reverse ? pl.ns - 1 - x : x; };
-        auto load_sum = [&](int x, f32x4 (&to)[TT][NT]) {
+        auto load_sum = [&](int x, f32x4 (&to)[TT]) {
             const size_t index = ((size_t)(u - pl.s + number(x)) * b.H + h) * set.slices + slice;
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    // (a transposed sum holds the state's own rows and columns only)
-                    to[t][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    if (16 * t + 4 * lg < w.Da && col0 + mcol + 4 * nt < w.Dc) to[t][nt] = *fragments(w.u, index, t, nt);
-                }
+            for (int t = 0; t < TT; ++t) {
+                // (a transposed sum holds the state's own rows and columns only)
+                to[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (16 * t + 4 * lg < w.Da && col0 + lr < w.Dc) to[t] = *fragments(w.u, index, t);
+            }
         };
-        auto add_sum = [&](int x, const f32x4 (&from)[TT][NT]) {
+        auto add_sum = [&](int x, const f32x4 (&from)[TT]) {
             const float f = decay_power(g, min(b.seg, pl.seq_len - number(x) * b.seg));
 #pragma unroll
             for (int t = 0; t < TT; ++t)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) E[t][nt][r] = f * E[t][nt][r] + from[t][nt][r];
+                for (int r = 0; r < 4; ++r) E[t][r] = f * E[t][r] + from[t][r];
         };
         for (int x = 0; x < before; x += 2) {
-            f32x4 U0[TT][NT], U1[TT][NT];
+            f32x4 U0[TT], U1[TT];
             load_sum(x, U0);
             if (x + 1 < before) load_sum(x + 1, U1);
             add_sum(x, U0);
@@ -527,7 +510,7 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     }
     const float lam16 = CI > 2 ? lam(16) : 1.f, lam32 = CI > 2 ? lam(32) : 1.f;
     const int oes = w.out_f32 ? 4 : T::bytes;
-    const int fo = col0 + 4 * NT * lg < w.Dc ? rsgn * lr * (b.H * w.Dc * oes) + (col0 + 4 * NT * lg) * oes : kFar;
+    const int fo = col0 + 4 * lg < w.Dc ? rsgn * lr * (b.H * w.Dc * oes) + (col0 + 4 * lg) * oes : kFar;
     const bool weighted = DG && w.x.p && !w.reverse;  // the walk that sums (i - j) times the pairs
     double dg = 0.0;
     if (!early && chunks > 0) fetch(0);
@@ -548,38 +531,35 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
         mx::barrier_lds();
         // the state that dq's walk kept of this chunk, on the way while the pairs and the state's read are formed
         const size_t kept_at = ((size_t)(pl.chunk0 + ci) * b.H + h) * set.slices + slice;
-        f32x4 kept[DG ? TT : 1][NT];
+        f32x4 kept[DG ? TT : 1];
         if constexpr (DG) {
             if (w.chunk_e && w.reverse) {
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) kept[t][nt] = *fragments(w.chunk_e, kept_at, t, nt);
+                    kept[t] = *fragments(w.chunk_e, kept_at, t);
             }
         }
-        // and the lane's part of the rows of x: four channels of each token and column tile
-        f32x4 xr[DG ? CI : 1][NT];
+        // and the lane's part of the rows of x: four channels of each token
+        f32x4 xr[DG ? CI : 1];
         if constexpr (DG) {
             if (w.x.p) {
                 const char *px = view(w.x);
 #pragma unroll
-                for (int I = 0; I < CI; ++I)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int i = 16 * I + lr, col = col0 + 4 * NT * lg + 4 * nt;
-                        xr[I][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-                        if (i < n && col < w.Dc) {
-                            const int64_t row = ci * CH + (w.reverse ? n - 1 - i : i);
-                            const char *at = px + row * w.x.tok + (int64_t)col * T::bytes;
-                            if constexpr (BF16) {
-                                const uint2 y = *reinterpret_cast<const uint2 *>(at);
-                                xr[I][nt] = f32x4{__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u),
-                                                  __uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u)};
-                            } else {
-                                xr[I][nt] = *reinterpret_cast<const f32x4 *>(at);
-                            }
+                for (int I = 0; I < CI; ++I) {
+                    const int i = 16 * I + lr, col = col0 + 4 * lg;
+                    xr[I] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    if (i < n && col < w.Dc) {
+                        const int64_t row = ci * CH + (w.reverse ? n - 1 - i : i);
+                        const char *at = px + row * w.x.tok + (int64_t)col * T::bytes;
+                        if constexpr (BF16) {
+                            const uint2 y = *reinterpret_cast<const uint2 *>(at);
+                            xr[I] = f32x4{__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u),
+                                              __uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u)};
+                        } else {
+                            xr[I] = *reinterpret_cast<const f32x4 *>(at);
                         }
                     }
+                }
             }
         }
 
@@ -629,40 +609,31 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
             }
         }
 
-        f32x4 O[CI][NT];
+        f32x4 O[CI];
         if constexpr (OUT) {
             // the state's read, transposed: rows c's channels, columns tokens.  From here to the barrier a
             // wavefront is mostly products: it goes first (the prefill walk's passes 122 -> 118 us)
             __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int I = 0; I < CI; ++I)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) O[I][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                O[I] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kb = 0; kb < KD; ++kb) {
-                frag hi[NT], lo[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (BF16) split_tiles(E[2 * kb][nt], E[2 * kb + 1][nt], hi[nt], lo[nt]);
-                    else hi[nt] = E[kb][nt];
-                }
+                frag hi, lo;
+                if constexpr (BF16) split_tiles(E[2 * kb], E[2 * kb + 1], hi, lo);
+                else hi = E[kb];
 #pragma unroll
                 for (int I = 0; I < CI; ++I) {
                     const frag af = row_frag<BF16, kRows, TileA>(sm.a, 16 * I + lr, kb, lg);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        O[I][nt] = mul_add(hi[nt], af, O[I][nt]);
-                        if constexpr (BF16) O[I][nt] = mul_add(lo[nt], af, O[I][nt]);
-                    }
+                    O[I] = mul_add(hi, af, O[I]);
+                    if constexpr (BF16) O[I] = mul_add(lo, af, O[I]);
                 }
             }
 #pragma unroll
             for (int I = 0; I < CI; ++I) {
                 const float f = lam(16 * I + lr) * w.oscale;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) O[I][nt][r] *= f;
+                for (int r = 0; r < 4; ++r) O[I][r] *= f;
             }
         }
 
@@ -670,16 +641,14 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
             if (w.chunk_e) {
                 float sum = 0.f;
 #pragma unroll
-                for (int t = 0; t < TT; ++t)
+                for (int t = 0; t < TT; ++t) {
+                    if (!w.reverse) {
+                        *fragments(w.chunk_e, kept_at, t) = E[t];
+                    } else {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (!w.reverse) {
-                            *fragments(w.chunk_e, kept_at, t, nt) = E[t][nt];
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) sum += kept[t][nt][r] * E[t][nt][r];
-                        }
+                        for (int r = 0; r < 4; ++r) sum += kept[t][r] * E[t][r];
                     }
+                }
                 // pairs across the whole chunk: n lambda^n <S, R>, and the stored E is lambda S
                 if (w.reverse) dg += static_cast<double>(sum) * static_cast<double>(n * lam(n - 1));
             }
@@ -689,16 +658,13 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
 #pragma unroll
             for (int t = 0; t < TT; ++t)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) E[t][nt][r] *= f;
+                for (int r = 0; r < 4; ++r) E[t][r] *= f;
         }
-        f32x4 Y[DG ? CI : 1][NT];
+        f32x4 Y[DG ? CI : 1];
         if constexpr (DG)
 #pragma unroll
             for (int I = 0; I < CI; ++I)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) Y[I][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                Y[I] = f32x4{0.f, 0.f, 0.f, 0.f};
         if constexpr (DG) {
             // the state's part of <x, out>, token i weighted by its distance to the chunk's start (in the
             // direction that the pairs decay)
@@ -710,53 +676,44 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
                     const float f = static_cast<float>(w.reverse ? i : i + 1);
                     if (i < n) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (col0 + 4 * NT * lg + 4 * nt < w.Dc) sum += f * xr[I][nt][r] * O[I][nt][r];
+                        for (int r = 0; r < 4; ++r)
+                            if (col0 + 4 * lg < w.Dc) sum += f * xr[I][r] * O[I][r];
                     }
                 }
                 dg += static_cast<double>(sum);
             }
         }
         // (c is read twice, here and behind the barrier: kept, it would not fit the registers)
-        auto c_frags = [&](int kb, frag (&to)[NT]) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) to[nt] = col_frag<BF16>(sm.c, LDC, wv * 16 * NT + 16 * nt, kb, lr, lg);
+        auto c_frags = [&](int kb, frag &to) {
+            to = col_frag<BF16>(sm.c, LDC, wv * 16, kb, lr, lg);
         };
         if (update) {
 #pragma unroll
             for (int kb = 0; kb < KT; ++kb) {
-                frag cf[NT], wh[NT], wm[NT], wl[NT];
+                frag cf, wh, wm, wl;
                 c_frags(kb, cf);
                 f32x4 wj[T::depth / 16];
 #pragma unroll
                 for (int y = 0; y < T::depth / 16; ++y)
                     wj[y] = *reinterpret_cast<const f32x4 *>(sm.write + T::depth * kb + 16 * y + 4 * lg);
+                if constexpr (BF16) {
+                    float y[8];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (BF16) {
-                        float y[8];
+                    for (int e = 0; e < 8; ++e) y[e] = static_cast<float>(cf[e]) * wj[e / 4][e % 4];
+                    split8x3(y, wh, wm, wl);
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = static_cast<float>(cf[nt][e]) * wj[e / 4][e % 4];
-                        split8x3(y, wh[nt], wm[nt], wl[nt]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) wh[nt][e] = cf[nt][e] * wj[0][e];
-                    }
+                    for (int e = 0; e < 4; ++e) wh[e] = cf[e] * wj[0][e];
                 }
                 frag bt = col_frag<BF16>(sm.b, LDB, 0, kb, lr, lg);
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
                     const frag now = bt;
                     if (t + 1 < TT) bt = col_frag<BF16>(sm.b, LDB, 16 * (t + 1), kb, lr, lg);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) E[t][nt] = mul_add(now, wh[nt], E[t][nt]);
+                    E[t] = mul_add(now, wh, E[t]);
                     if constexpr (BF16) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) E[t][nt] = mul_add(now, wm[nt], E[t][nt]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) E[t][nt] = mul_add(now, wl[nt], E[t][nt]);
+                        E[t] = mul_add(now, wm, E[t]);
+                        E[t] = mul_add(now, wl, E[t]);
                     }
                 }
             }
@@ -767,24 +724,21 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
             mx::barrier_lds();  // the pair matrix is written
 #pragma unroll
             for (int kb = 0; kb < KT; ++kb) {
-                frag cf[NT];
+                frag cf;
                 c_frags(kb, cf);
 #pragma unroll
                 for (int I = 0; I < CI; ++I) {
                     if (BF16 ? kb <= (I >> 1) : kb <= I) {
                         const int at = (pair_frag<BF16, CI>(I, kb) * 64 + lane) * 16;
                         const frag pf = *reinterpret_cast<const frag *>(sm.p + at);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) O[I][nt] = mul_add(cf[nt], pf, O[I][nt]);
+                        O[I] = mul_add(cf, pf, O[I]);
                         if constexpr (DG) {
                             if (weighted) {
                                 const frag qh = *reinterpret_cast<const frag *>(sm.ph + at);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) Y[I][nt] = mul_add(cf[nt], qh, Y[I][nt]);
+                                Y[I] = mul_add(cf, qh, Y[I]);
                                 if constexpr (BF16) {
                                     const frag ql = *reinterpret_cast<const frag *>(sm.pl + at);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) Y[I][nt] = mul_add(cf[nt], ql, Y[I][nt]);
+                                    Y[I] = mul_add(cf, ql, Y[I]);
                                 }
                             }
                         }
@@ -803,30 +757,17 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
                 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
                 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
                 if (!BF16 || w.out_f32) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[I][nt]), ro,
-                                                               (int)(off + 16 * nt), 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[I]), ro, (int)off, 0, 0);
                 } else {
-                    uint32_t v[2 * NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        v[2 * nt] = pack2(O[I][nt][0], O[I][nt][1]);
-                        v[2 * nt + 1] = pack2(O[I][nt][2], O[I][nt][3]);
-                    }
-                    if constexpr (NT == 2)
-                        __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[0], v[1], v[2], v[3]}, ro, (int)off, 0, 0);
-                    else
-                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, ro, (int)off, 0, 0);
+                    const u32x2 v = {pack2(O[I][0], O[I][1]), pack2(O[I][2], O[I][3])};
+                    __builtin_amdgcn_raw_buffer_store_b64(v, ro, (int)off, 0, 0);
                 }
                 if constexpr (DG) {
                     if (weighted && 16 * I + lr < n) {
                         float sum = 0.f;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (col0 + 4 * NT * lg + 4 * nt < w.Dc) sum += xr[I][nt][r] * Y[I][nt][r];
+                        for (int r = 0; r < 4; ++r)
+                            if (col0 + 4 * lg < w.Dc) sum += xr[I][r] * Y[I][r];
                         dg += static_cast<double>(sum);
                     }
                 }
@@ -836,40 +777,35 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
 
     if constexpr (!OUT) {
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+        for (int t = 0; t < TT; ++t) {
+            *fragments(w.u, part, t) = E[t];
+            if (w.u_t) {
+                // element (row, col) as (col, row) of the other walk's fragments
+                const int row = 16 * t + 4 * lg, col = col0 + lr;
+                const int ws = row / COLS, ww = row % COLS / 16, cc = row % 16;
+                float *to = w.u_t + (((size_t)u * b.H + h) * set.slices + ws) * (size_t)(PAD * COLS) +
+                            (((size_t)ww * TT + (col >> 4)) * 64 + (col >> 2 & 3) * 16 + cc) * 4 + (col & 3);
+                if (row < w.Da && col < w.Dc) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                *fragments(w.u, part, t, nt) = E[t][nt];
-                if (w.u_t) {
-                    // element (row, col) as (col, row) of the other walk's fragments
-                    const int row = 16 * t + 4 * lg, col = col0 + mcol + 4 * nt;
-                    const int ws = row / COLS, ww = row % COLS / (16 * NT), cc = row % (16 * NT);
-                    float *to = w.u_t + (((size_t)u * b.H + h) * set.slices + ws) * (size_t)(PAD * COLS) +
-                                ((((size_t)ww * TT + (col >> 4)) * NT + (cc >> 2) % NT) * 64 + (col >> 2 & 3) * 16 +
-                                 4 * (cc / (4 * NT))) * 4 + (col & 3);
-                    if (row < w.Da && col < w.Dc) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) to[4 * r] = E[t][nt][r];
-                    }
+                    for (int r = 0; r < 4; ++r) to[4 * r] = E[t][r];
                 }
             }
+        }
     } else {
         if (w.ef && last_seg) {
             // an empty sequence keeps its state: E holds e0, decayed in the forward direction
             const bool empty = pl.seq_len == 0;
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
+            for (int t = 0; t < TT; ++t) {
+                const int row = 16 * t + 4 * lg, col = col0 + lr;
+                if (row < w.Da && col < w.Dc) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int row = 16 * t + 4 * lg, col = col0 + mcol + 4 * nt;
-                    if (row < w.Da && col < w.Dc) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const size_t at = e_base + (size_t)(row + r) * w.Dc + col;
-                            w.ef[at] = empty ? (w.e0 ? w.e0[at] : 0.f) : E[t][nt][r];
-                        }
+                    for (int r = 0; r < 4; ++r) {
+                        const size_t at = e_base + (size_t)(row + r) * w.Dc + col;
+                        w.ef[at] = empty ? (w.e0 ? w.e0[at] : 0.f) : E[t][r];
                     }
                 }
+            }
         }
         if constexpr (DG) {
             if (w.dg_part) {
@@ -888,10 +824,10 @@ __global__ __launch_bounds__(64 * WV, WV == 8 && MODE != kWalkDg ? 4 : 2) void w
     }
 }
 
-template <bool BF16, int PAD, int NT, int CH, int WV, int MODE>
+template <bool BF16, int PAD, int CH, int WV, int MODE>
 hipError_t launch(const WalkSet &s, hipStream_t stream) {
     const dim3 grid((unsigned)(s.b.units * s.b.H * s.slices), (unsigned)s.count);
-    hipLaunchKernelGGL((walk_kernel<BF16, PAD, NT, CH, WV, MODE>), grid, dim3(64 * WV), 0, stream, s);
+    hipLaunchKernelGGL((walk_kernel<BF16, PAD, CH, WV, MODE>), grid, dim3(64 * WV), 0, stream, s);
     return hipGetLastError();
 }
 
@@ -899,16 +835,16 @@ template <int MODE>
 hipError_t dispatch(const WalkSet &s, bool bf16, const Shape &sh, hipStream_t stream) {
     if (bf16) {
         if (sh.pad == 64)
-            return sh.cols == 64 ? launch<true, 64, 1, 64, 4, MODE>(s, stream) : launch<true, 64, 1, 64, 8, MODE>(s, stream);
+            return sh.cols == 64 ? launch<true, 64, 64, 4, MODE>(s, stream) : launch<true, 64, 64, 8, MODE>(s, stream);
         if (sh.pad == 128)
-            return sh.cols == 64 ? launch<true, 128, 1, 64, 4, MODE>(s, stream) : launch<true, 128, 1, 64, 8, MODE>(s, stream);
-        return launch<true, 256, 1, 32, 4, MODE>(s, stream);
+            return sh.cols == 64 ? launch<true, 128, 64, 4, MODE>(s, stream) : launch<true, 128, 64, 8, MODE>(s, stream);
+        return launch<true, 256, 32, 4, MODE>(s, stream);
     }
     if (sh.pad == 64)
-        return sh.cols == 64 ? launch<false, 64, 1, 32, 4, MODE>(s, stream) : launch<false, 64, 1, 32, 8, MODE>(s, stream);
+        return sh.cols == 64 ? launch<false, 64, 32, 4, MODE>(s, stream) : launch<false, 64, 32, 8, MODE>(s, stream);
     if (sh.pad == 128)
-        return sh.cols == 64 ? launch<false, 128, 1, 32, 4, MODE>(s, stream) : launch<false, 128, 1, 32, 8, MODE>(s, stream);
-    return launch<false, 256, 1, 32, 4, MODE>(s, stream);
+        return sh.cols == 64 ? launch<false, 128, 32, 4, MODE>(s, stream) : launch<false, 128, 32, 8, MODE>(s, stream);
+    return launch<false, 256, 32, 4, MODE>(s, stream);
 }
 
 // ---- sums over the query heads of a group, and of dL/dg's parts
